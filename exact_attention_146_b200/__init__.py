@@ -2,7 +2,8 @@
 
 Forward (fa_fwd: bf16 / fp16, causal or sliding window, split-KV; fa_fwd_fp8: E4M3),
 key-shard partials and their merge (fa_fwd_partial, fa_merge_partials; see kshard for the
-multi-GPU exchange) and the backward pass (fa_bwd).
+multi-GPU exchange) and the backward pass (fa_bwd).  Paged key/value caches (block tables,
+rotary embedding into the cache, attention over it) are in paged and exported here.
 
 This module only marshals arguments (torch tensors -> device pointers, sizes and the
 current CUDA stream) into the C ABI declared in ``include/fa.h``; every step of the
@@ -18,7 +19,8 @@ from pathlib import Path
 __all__ = ["fa_fwd", "fa_fwd_fp8", "fa_fwd_partial", "fa_merge_partials", "fa_bwd", "fa_fwd_raw",
            "splitkv_workspace_bytes", "splitkv_default_splits", "bwd_workspace_bytes", "device_status",
            "tile_config", "status_string", "FaError", "lib", "SUPPORTED_HEAD_DIMS", "BWD_HEAD_DIMS", "LIB_PATH",
-           "withheld_load_forward"]
+           "withheld_load_forward", "RopeTable", "PagedKV", "fa_kv_reserve", "fa_kv_release", "fa_rope", "fa_rope_append",
+           "fa_paged_fwd", "paged_workspace_bytes"]
 
 LIB_PATH = Path(__file__).resolve().parent / "libfa.so"
 SUPPORTED_HEAD_DIMS = (32, 64, 80, 96, 128, 192, 256)   # forward
@@ -34,11 +36,13 @@ FA_ERR_DEVICE_TIMEOUT = 6
 FA_ERR_NOT_DEVICE_MEMORY = 7
 FA_ERR_OVERLAP = 8
 FA_ERR_SCRATCH_LIMIT = 9
+FA_ERR_PAGED_RANGE = 10
 SPLITKV_STATIC_SCRATCH_BYTES = 16 * 1024 * 1024
 
 EXPORTED = ("fa_fwd", "fa_fwd_window", "fa_fwd_splitkv", "fa_splitkv_workspace_bytes", "fa_splitkv_default_splits",
             "fa_fwd_splitkv_static", "fa_fwd_f16", "fa_fwd_fp8", "fa_fwd_partial", "fa_merge_partials", "fa_bwd", "fa_bwd_f16", "fa_bwd_window", "fa_bwd_workspace_bytes", "fa_status_string", "fa_device_status", "fa_tile_config", "fa_version",
-            "fa_test_withheld_load", "fa_fwd_window_f16", "fa_fwd_splitkv_f16")
+            "fa_test_withheld_load", "fa_fwd_window_f16", "fa_fwd_splitkv_f16", "fa_kv_reserve", "fa_kv_release", "fa_rope", "fa_rope_f16",
+            "fa_rope_append", "fa_rope_append_f16", "fa_paged_workspace_bytes", "fa_paged_fwd", "fa_paged_fwd_f16")
 
 
 class FaError(RuntimeError):
@@ -100,6 +104,7 @@ def lib() -> ctypes.CDLL:
         L.fa_tile_config.restype = ci
         L.fa_version.argtypes = []
         L.fa_version.restype = ci
+        paged.declare(L)
         _lib = L
     return _lib
 
@@ -340,3 +345,8 @@ def device_status(stream=None) -> tuple[int, int]:
     detail = ctypes.c_int(0)
     rc = lib().fa_device_status(_stream_handle(stream), ctypes.byref(detail))
     return rc, detail.value
+
+
+from . import paged  # noqa: E402  (uses the names above)
+from .paged import (PagedKV, RopeTable, fa_kv_release, fa_kv_reserve, fa_paged_fwd, fa_rope, fa_rope_append,  # noqa: E402
+                    paged_workspace_bytes)

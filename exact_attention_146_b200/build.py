@@ -17,7 +17,7 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 LIB = PKG / "libfa.so"
-SOURCES = [CSRC / "fa_fwd.cu", CSRC / "fa_bwd.cu"]
+SOURCES = [CSRC / n for n in ("fa_fwd.cu", "fa_bwd.cu", "fa_tables.cu", "fa_rope.cu", "fa_paged.cu")]
 DEPS = SOURCES + sorted(CSRC.glob("*.cuh")) + sorted(CSRC.glob("*.h")) + sorted(INCLUDE.glob("*.h"))
 
 NVCC_FLAGS = [

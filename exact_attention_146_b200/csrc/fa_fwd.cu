@@ -108,6 +108,13 @@ int check_device_range(const void *p, size_t bytes, int dev) {
     return FA_OK;
 }
 
+int check_spans(const Span *s, int n, int dev) {
+    for (int i = 0; i < n; ++i)
+        if (s[i].bytes > 0)
+            if (const int rc = check_device_range(s[i].p, s[i].bytes, dev)) return rc;
+    return FA_OK;
+}
+
 bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
     if (a == nullptr || b == nullptr || na == 0 || nb == 0) return false;
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
@@ -358,6 +365,9 @@ const char *fa_status_string(int status) {
         case FA_ERR_SCRATCH_LIMIT:
             return "the split-KV partials need more than the library's 16 MiB static scratch: use "
                    "fa_fwd_splitkv with a caller workspace, or fewer splits";
+        case FA_ERR_PAGED_RANGE:
+            return "a length, block-table entry, free-stack entry or slot that a kernel read on the device is out "
+                   "of range, or a step needs more blocks or tokens than there is room for";
         default: return "unknown status";
     }
 }

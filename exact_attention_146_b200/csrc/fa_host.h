@@ -4,10 +4,13 @@
 #pragma once
 
 #include <cstddef>
+#include <cstdint>
 #include <mutex>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+
+#include "fa.h"
 
 namespace fa_host {
 
@@ -39,6 +42,32 @@ int current_device(DeviceState **out, int *dev_out);
 // `bytes` starting at `p` must be device (or managed) memory of device `dev`, inside one allocation.
 int check_device_range(const void *p, size_t bytes, int dev);
 bool overlaps(const void *a, size_t na, const void *b, size_t nb);
+
+// One array of an entry point: where it starts, its bytes (0: empty, not looked at), its alignment.
+struct Span {
+    const void *p;
+    size_t bytes;
+    uintptr_t align;
+};
+// Host-only checks of an entry point's arrays: alignment, and that no output overlaps an input or
+// another output.  same(i, o): input i and output o may be the same array (an in-place update).
+template <class Same>
+int check_layout(const Span *in, int n_in, const Span *out, int n_out, Same same) {
+    for (int i = 0; i < n_in; ++i)
+        if (in[i].bytes > 0 && reinterpret_cast<uintptr_t>(in[i].p) % in[i].align != 0) return FA_ERR_MISALIGNED;
+    for (int o = 0; o < n_out; ++o)
+        if (out[o].bytes > 0 && reinterpret_cast<uintptr_t>(out[o].p) % out[o].align != 0) return FA_ERR_MISALIGNED;
+    for (int o = 0; o < n_out; ++o) {
+        for (int i = 0; i < n_in; ++i)
+            if (overlaps(out[o].p, out[o].bytes, in[i].p, in[i].bytes) && !same(i, o)) return FA_ERR_OVERLAP;
+        for (int u = 0; u < o; ++u)
+            if (overlaps(out[o].p, out[o].bytes, out[u].p, out[u].bytes)) return FA_ERR_OVERLAP;
+    }
+    return FA_OK;
+}
+// check_device_range of every array that is not empty.
+int check_spans(const Span *s, int n, int dev);
+
 // 4-D view (d, H, N, B) of a [B, N, H, d] tensor, box (cw, heads, rows, 1); elem: 0 bf16,
 // 1 fp16, 2 E4M3 bytes.
 int encode_bnhd(CUtensorMap *m, const void *base, int d, int H, int N, int B, int cw, int rows, int heads = 1,

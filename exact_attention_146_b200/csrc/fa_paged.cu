@@ -1,0 +1,181 @@
+// fa_paged.cu -- attention of new tokens over a paged cache (fa_paged_fwd, declared in include/fa.h):
+// argument checks, workspace layout and launches of the kernels in fa_paged_rows.cuh.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "fa.h"
+#include "fa_cache.h"
+#include "fa_host.h"
+#include "fa_paged_rows.cuh"
+
+namespace {
+
+using namespace fa;
+using namespace fa_host;
+
+constexpr int kMaxRowWorkers = kMaxPagedCtas * 8;
+
+size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
+
+// Workspace: the pieces' O (fp32), then their LSE; two pieces a worker at most (its range's first
+// and last unit).
+size_t part_o_bytes(int workers, int rows, int d) { return align256(size_t(workers) * 2 * rows * d * 4); }
+size_t part_bytes(int workers, int rows, int d) { return part_o_bytes(workers, rows, d) + align256(size_t(workers) * 2 * rows * 4); }
+
+int largest_divisor(int n, int most) {
+    for (int x = std::min(n, most); x > 1; --x)
+        if (n % x == 0) return x;
+    return 1;
+}
+
+// Launches `kern` so that its blocks may be set up while the kernel before it in the stream still
+// runs (it waits for that kernel's end itself, by griddepcontrol.wait).
+template <class P>
+int launch_after(void (*kern)(P), dim3 grid, int threads, const P &p, cudaStream_t st) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
+        cudaGetLastError();
+        return FA_ERR_CUDA;
+    }
+    return FA_OK;
+}
+
+template <class C>
+int launch_rows(PagedParams p, void *workspace, int ctas, int dev, cudaStream_t st) {
+    static bool smem_set[kMaxDevices] = {};
+    {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        if (!smem_set[dev]) {
+            if (cudaFuncSetAttribute(fa_paged_rows_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) {
+                cudaGetLastError();
+                return FA_ERR_CUDA;
+            }
+            smem_set[dev] = true;
+        }
+    }
+    const int workers = ctas * C::WARPS;
+    p.pack = largest_divisor(p.n_rep, kRowRows);
+    p.plan.groups = p.Hq / p.pack;
+    p.plan.tpb = kRowRows / p.pack;
+    p.plan.workers = workers;
+    p.o_part = static_cast<float *>(workspace);
+    p.lse_part = reinterpret_cast<float *>(static_cast<char *>(workspace) + part_o_bytes(workers, kRowRows, C::D));
+    fa_paged_rows_kernel<C><<<unsigned(ctas), C::THREADS, C::SMEM, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    return launch_after(fa_paged_merge_kernel<C::D, C::F16, kRowRows, kRowKeys>, dim3(unsigned(workers - 1)), 128, p, st);
+}
+
+template <bool F16>
+int dispatch(const PagedParams &p, int d, void *workspace, int ctas, int dev, cudaStream_t st) {
+    switch (d) {
+        case 32: return launch_rows<RowCfg<32, F16>>(p, workspace, ctas, dev, st);
+        case 64: return launch_rows<RowCfg<64, F16>>(p, workspace, ctas, dev, st);
+        case 80: return launch_rows<RowCfg<80, F16>>(p, workspace, ctas, dev, st);
+        case 96: return launch_rows<RowCfg<96, F16>>(p, workspace, ctas, dev, st);
+        case 128: return launch_rows<RowCfg<128, F16>>(p, workspace, ctas, dev, st);
+        case 192: return launch_rows<RowCfg<192, F16>>(p, workspace, ctas, dev, st);
+        default: return launch_rows<RowCfg<256, F16>>(p, workspace, ctas, dev, st);
+    }
+}
+
+int paged_fwd(const void *q, long long q_stride, const fa_paged_cache *cache, const int *block_table,
+              long long table_stride, int max_blocks, const int *cu_seqlens, const int *seq_lens, int R, int T, int Hq,
+              int max_new, float scale, int causal, int window, void *out, float *lse, void *workspace,
+              size_t workspace_bytes, bool f16, void *stream) {
+    // ---- host-only validation
+    if (cache == nullptr || R < 0 || T < 0 || Hq <= 0 || Hq > 65535 || max_new < 0 || max_blocks < 0) return FA_ERR_INVALID_ARG;
+    int rc = valid_cache(cache);
+    if (rc != FA_OK) return rc;
+    const int d = cache->d, Hkv = cache->Hkv;
+    if (Hq % Hkv != 0 || (causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal)) return FA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
+    if (table_stride < max_blocks || (long long)max_blocks * cache->page_size > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+    if (q_stride < (long long)Hq * d || q_stride % 8 != 0) return FA_ERR_INVALID_ARG;
+    if (R == 0 || T == 0) return FA_OK;
+    const size_t q_b = (size_t(T - 1) * size_t(q_stride) + size_t(Hq) * d) * 2, out_b = size_t(T) * Hq * d * 2;
+    const size_t lse_b = lse != nullptr ? size_t(T) * Hq * 4 : 0, kv_b = cache_bytes(cache);
+    const size_t tab_b = max_blocks > 0 ? (size_t(R - 1) * size_t(table_stride) + size_t(max_blocks)) * 4 : 0;
+    const size_t ws_b = fa_paged_workspace_bytes(Hq, Hkv, d);
+    if (q == nullptr || out == nullptr || cu_seqlens == nullptr || seq_lens == nullptr) return FA_ERR_INVALID_ARG;
+    if ((tab_b > 0 && block_table == nullptr) || (kv_b > 0 && (cache->k == nullptr || cache->v == nullptr))) return FA_ERR_INVALID_ARG;
+    if (workspace == nullptr || workspace_bytes < ws_b) return FA_ERR_INVALID_ARG;
+    const Span in[] = {{q, q_b, 16}, {cache->k, kv_b, 16}, {cache->v, kv_b, 16}, {block_table, tab_b, 4},
+                       {cu_seqlens, (size_t(R) + 1) * 4, 4}, {seq_lens, size_t(R) * 4, 4}};
+    const Span outs[] = {{out, out_b, 16}, {lse, lse_b, 4}, {workspace, ws_b, 256}};
+    if ((rc = check_layout(in, 6, outs, 3, [](int, int) { return false; })) != FA_OK) return rc;
+
+    // ---- device checks
+    DeviceState *dev = nullptr;
+    int dev_id = -1;
+    if ((rc = current_device(&dev, &dev_id)) != FA_OK) return rc;
+    if ((rc = check_spans(in, 6, dev_id)) != FA_OK || (rc = check_spans(outs, 3, dev_id)) != FA_OK) return rc;
+
+    PagedParams p{};
+    p.plan.cu = cu_seqlens;
+    p.plan.lens = seq_lens;
+    p.plan.status = dev->status_ptr;
+    p.plan.max_len = (long long)max_blocks * cache->page_size;
+    p.plan.R = R;
+    p.plan.T = T;
+    p.plan.max_new = max_new;
+    p.plan.causal = causal;
+    p.plan.window = window;
+    p.q = static_cast<const uint16_t *>(q);
+    p.k = static_cast<const uint16_t *>(cache->k);
+    p.v = static_cast<const uint16_t *>(cache->v);
+    p.out = static_cast<uint16_t *>(out);
+    p.lse = lse;
+    p.table = block_table;
+    p.table_stride = table_stride;
+    p.q_stride = q_stride;
+    p.block_stride = cache->block_stride;
+    p.slot_stride = cache->slot_stride;
+    p.head_stride = cache->head_stride;
+    p.Hq = Hq;
+    p.n_rep = Hq / Hkv;
+    p.page = cache->page_size;
+    p.num_blocks = cache->num_blocks;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    const int ctas = std::min(dev->num_sms, kMaxPagedCtas);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return f16 ? dispatch<true>(p, d, workspace, ctas, dev_id, st) : dispatch<false>(p, d, workspace, ctas, dev_id, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fa_paged_workspace_bytes(int Hq, int Hkv, int d) {
+    if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || fa_tile_config(d, nullptr, nullptr, nullptr, nullptr) != FA_OK) return 0;
+    return part_bytes(kMaxRowWorkers, kRowRows, d);
+}
+
+int fa_paged_fwd(const void *q, long long q_stride, const fa_paged_cache *cache, const int *block_table,
+                 long long table_stride, int max_blocks, const int *cu_seqlens, const int *seq_lens, int R, int T, int Hq,
+                 int max_new, float scale, int causal, int window, void *out, float *lse, void *workspace,
+                 size_t workspace_bytes, void *stream) {
+    return paged_fwd(q, q_stride, cache, block_table, table_stride, max_blocks, cu_seqlens, seq_lens, R, T, Hq, max_new,
+                     scale, causal, window, out, lse, workspace, workspace_bytes, false, stream);
+}
+
+int fa_paged_fwd_f16(const void *q, long long q_stride, const fa_paged_cache *cache, const int *block_table,
+                     long long table_stride, int max_blocks, const int *cu_seqlens, const int *seq_lens, int R, int T,
+                     int Hq, int max_new, float scale, int causal, int window, void *out, float *lse, void *workspace,
+                     size_t workspace_bytes, void *stream) {
+    return paged_fwd(q, q_stride, cache, block_table, table_stride, max_blocks, cu_seqlens, seq_lens, R, T, Hq, max_new,
+                     scale, causal, window, out, lse, workspace, workspace_bytes, true, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,364 @@
+"""Serving many requests from one paged key/value cache: block tables and slots built on the GPU
+(fa_kv_reserve, fa_kv_release), rotary position embedding with several axes (fa_rope, and
+fa_rope_append, which also writes the cache) and attention over the cache (fa_paged_fwd).
+PagedKV keeps the state of such a cache and runs the four in order.
+
+As in the rest of the binding, the functions marshal arguments into the C ABI of
+``include/fa.h``; all lengths, tables and counts stay on the device, no call synchronises, and
+everything can be captured in a CUDA graph when the output buffers are given."""
+from __future__ import annotations
+
+import ctypes
+import math
+
+__all__ = ["RopeTable", "PagedKV", "fa_kv_reserve", "fa_kv_release", "fa_rope", "fa_rope_append", "fa_paged_fwd",
+           "paged_workspace_bytes"]
+
+
+class _RopeSpec(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("num_axes", ctypes.c_int),
+                ("inv_freq", ctypes.POINTER(ctypes.c_double)), ("axis", ctypes.POINTER(ctypes.c_int))]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("block_stride", ctypes.c_longlong),
+                ("slot_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong), ("num_blocks", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int)]
+
+
+def declare(L) -> None:
+    """Argument types of the paged-cache entry points of the loaded library."""
+    vp, ci, ll, cf = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
+    L.fa_kv_reserve.argtypes = [vp, vp, ci, vp, ll, ci, vp, vp, ci, ci, ci, vp, vp, vp, vp, vp, vp]
+    L.fa_kv_release.argtypes = [vp, vp, ci, vp, ll, ci, vp, vp, ci, ci, vp, vp, vp]
+    rope = [vp, ll, vp, ll, ci, vp, ll, vp, ll, ci, ci, ci, vp, ll, ctypes.POINTER(_RopeSpec), ci, vp]
+    append = [vp, ll, vp, ll, ci, vp, ll, vp, ll, ci, vp, ll, ctypes.POINTER(_RopeSpec), ctypes.POINTER(_Cache), vp, vp]
+    paged = [vp, ll, ctypes.POINTER(_Cache), vp, ll, ci, vp, vp, ci, ci, ci, ci, cf, ci, ci, vp, vp, vp, ctypes.c_size_t, vp]
+    for name, args in (("fa_rope", rope), ("fa_rope_append", append), ("fa_paged_fwd", paged)):
+        for f16 in ("", "_f16"):
+            getattr(L, name + f16).argtypes = args
+            getattr(L, name + f16).restype = ci
+    L.fa_kv_reserve.restype = L.fa_kv_release.restype = ci
+    L.fa_paged_workspace_bytes.argtypes = [ci, ci, ci]
+    L.fa_paged_workspace_bytes.restype = ctypes.c_size_t
+
+
+def _core():
+    import exact_attention_146_b200 as fa
+    return fa
+
+
+def _run(name, stream, *args):
+    fa = _core()
+    rc = getattr(fa.lib(), name)(*args, fa._stream_handle(stream))
+    if rc != fa.FA_OK:
+        raise fa.FaError(rc, name)
+
+
+def _empty(shape, dtype, device, stream):
+    """A buffer made here for a call on `stream` (None: the current one)."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):   # so that its memory is not handed out again before that stream is done with it
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _ints(name, t, shape, dtype=None):
+    import torch
+    dtype = dtype or torch.int32
+    if t.dtype != dtype or not t.is_cuda or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    return t
+
+
+def _table(t, R):
+    import torch
+    if t.dtype != torch.int32 or not t.is_cuda or t.dim() != 2 or t.shape[0] != R or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"block_table must be an int32 CUDA tensor [{R}, max_blocks] with adjacent entries, got {t.dtype} {tuple(t.shape)}")
+    width = t.shape[1]
+    return t, (max(t.stride(0), width) if R > 1 else width), width
+
+
+def _rows(name, t, dtype, d=None):
+    """A [T, heads, d] tensor whose heads lie next to each other: (pointer, elements from token to token)."""
+    if t.dtype != dtype or not t.is_cuda or t.dim() != 3 or (d is not None and t.shape[2] != d):
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor [T, heads, d], got {t.dtype} {tuple(t.shape)}")
+    T, H, dd = t.shape
+    if (dd > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != dd):
+        raise ValueError(f"{name}: the heads of a token must lie next to each other, strides {tuple(t.stride())}")
+    return t.data_ptr(), (t.stride(0) if T > 1 else H * dd)
+
+
+def _cache(k, v):
+    """The C description of k and v caches, logically [blocks, slots, heads, d] with any strides of the first three."""
+    for name, t in (("k_cache", k), ("v_cache", v)):
+        if not t.is_cuda or t.dim() != 4 or t.dtype != k.dtype or (t.shape[3] > 1 and t.stride(3) != 1):
+            raise ValueError(f"{name} must be a 4-D CUDA tensor [blocks, slots, heads, d] with adjacent elements, got {t.dtype} {tuple(t.shape)}")
+    if k.shape != v.shape or k.stride() != v.stride():
+        raise ValueError(f"k_cache and v_cache must have the same shape and strides, got {tuple(k.shape)} {k.stride()} and {tuple(v.shape)} {v.stride()}")
+    blocks, page, heads, d = k.shape
+    return _Cache(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), blocks, page, heads, d)
+
+
+def _half(t):
+    import torch
+    if t.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"bf16 or fp16 expected, got {t.dtype}")
+    return "_f16" if t.dtype == torch.float16 else ""
+
+
+class RopeTable:
+    """Frequencies of a rotary embedding: inv_freq[i] and axis[i] of pair i (axis None: one axis);
+    interleaved pairs are (2i, 2i + 1), else (i, i + rot_dim / 2)."""
+
+    def __init__(self, inv_freq, axis=None, interleaved: bool = False):
+        inv = [float(x) for x in inv_freq]
+        axes = [0] * len(inv) if axis is None else [int(a) for a in axis]
+        if len(axes) != len(inv):
+            raise ValueError(f"{len(inv)} frequencies but {len(axes)} axes")
+        if not all(math.isfinite(x) for x in inv) or any(not 0 <= a < 4 for a in axes):
+            raise ValueError("frequencies must be finite, axes 0 .. 3")
+        self.rot_dim = 2 * len(inv)
+        self.num_axes = max(axes, default=0) + 1
+        self.interleaved = bool(interleaved)
+        self._inv = (ctypes.c_double * max(1, len(inv)))(*inv)
+        self._axis = (ctypes.c_int * max(1, len(inv)))(*axes)
+
+    def _spec(self, positions, T):
+        import torch
+        if positions.dim() == 1:
+            positions = positions[None]
+        n = positions.shape[0]
+        if positions.dtype != torch.int32 or not positions.is_cuda or positions.dim() != 2 or positions.shape[1] != T or \
+                (T > 1 and positions.stride(1) != 1):
+            raise ValueError(f"positions must be int32 CUDA [axes, {T}] (or [{T}]), got {positions.dtype} {tuple(positions.shape)}")
+        if n < self.num_axes:
+            raise ValueError(f"the table uses {self.num_axes} axes, positions has {n}")
+        spec = _RopeSpec(self.rot_dim, int(self.interleaved), n, self._inv, self._axis)
+        return spec, positions, (max(positions.stride(0), T) if n > 1 else T)
+
+
+def fa_rope(q, positions, table: RopeTable, *, k=None, inverse: bool = False, q_out=None, k_out=None, stream=None):
+    """Rotary embedding of q [T, Hq, d] (and k [T, Hkv, d]) bf16 or fp16 by positions [axes, T] int32;
+    inverse = True is its gradient (the opposite turn).  q and k may be slices of one projection.
+    Returns (q_out, k_out), or q_out alone without k; q_out may be q and k_out k (in place)."""
+    f16 = _half(q)
+    T, Hq, d = q.shape
+    qp, qs = _rows("q", q, q.dtype)
+    if q_out is None:
+        q_out = _empty((T, Hq, d), q.dtype, q.device, stream)
+    if tuple(q_out.shape) != (T, Hq, d):
+        raise ValueError(f"q_out must be {(T, Hq, d)}, got {tuple(q_out.shape)}")
+    qo, qos = _rows("q_out", q_out, q.dtype, d)
+    kp = ko = None
+    ks = kos = Hkv = 0
+    if k is not None:
+        if k.dim() != 3 or k.shape[0] != T:
+            raise ValueError(f"k must be [{T}, heads, {d}], got {tuple(k.shape)}")
+        kp, ks = _rows("k", k, q.dtype, d)
+        Hkv = k.shape[1]
+        if k_out is None:
+            k_out = _empty((T, Hkv, d), q.dtype, q.device, stream)
+        if tuple(k_out.shape) != (T, Hkv, d):
+            raise ValueError(f"k_out must be {(T, Hkv, d)}, got {tuple(k_out.shape)}")
+        ko, kos = _rows("k_out", k_out, q.dtype, d)
+    spec, pos, ps = table._spec(positions, T)
+    _run("fa_rope" + f16, stream, qp, qs, qo, qos, Hq, kp, ks, ko, kos, Hkv, T, d, pos.data_ptr(), ps, ctypes.byref(spec),
+         int(bool(inverse)))
+    return q_out if k is None else (q_out, k_out)
+
+
+def fa_rope_append(q, k, v, positions, table: RopeTable, k_cache, v_cache, slots, *, q_out=None, stream=None):
+    """Rotates q [T, Hq, d] and k [T, Hkv, d] and writes the rotated k and v [T, Hkv, d] to slots [T]
+    (int64, block * page_size + slot; negative: the row is left out) of the caches, logically
+    [blocks, slots, Hkv, d].  q may be None.  Returns q_out (rows without a slot as they were)."""
+    f16 = _half(k)
+    T, Hkv, d = k.shape
+    kp, ks = _rows("k", k, k.dtype)
+    vp, vs = _rows("v", v, k.dtype, d)
+    c = _cache(k_cache, v_cache)
+    if v.shape != k.shape or (c.Hkv, c.d) != (Hkv, d) or k_cache.dtype != k.dtype:
+        raise ValueError(f"shape mismatch k{tuple(k.shape)} v{tuple(v.shape)} cache{tuple(k_cache.shape)} {k_cache.dtype}")
+    import torch
+    _ints("slots", slots, (T,), torch.int64)
+    qp = qo = None
+    qs = qos = Hq = 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != T:
+            raise ValueError(f"q must be [{T}, heads, {d}], got {tuple(q.shape)}")
+        qp, qs = _rows("q", q, k.dtype, d)
+        Hq = q.shape[1]
+        if q_out is None:
+            q_out = _empty((T, Hq, d), q.dtype, q.device, stream)
+        if tuple(q_out.shape) != (T, Hq, d):
+            raise ValueError(f"q_out must be {(T, Hq, d)}, got {tuple(q_out.shape)}")
+        qo, qos = _rows("q_out", q_out, k.dtype, d)
+    spec, pos, ps = table._spec(positions, T)
+    _run("fa_rope_append" + f16, stream, qp, qs, qo, qos, Hq, kp, ks, vp, vs, T, pos.data_ptr(), ps, ctypes.byref(spec),
+         ctypes.byref(c), slots.data_ptr())
+    return q_out if q is not None else None
+
+
+def fa_kv_reserve(ctx_lens, new_lens, block_table, free_blocks, free_count, *, page_size: int, num_tokens: int | None = None,
+                  cu_seqlens=None, seq_lens=None, positions=None, slots=None, free_count_out=None, stream=None):
+    """Takes the blocks that R requests need for new_lens more tokens (fa_kv_reserve): fills
+    block_table [R, max_blocks] and returns (cu_seqlens [R + 1], seq_lens [R], positions [T], slots [T]
+    int64, free_count_out [1]).  T is given by num_tokens, or by positions or slots.  seq_lens may be
+    ctx_lens and free_count_out free_count (updated in place)."""
+    import torch
+    R = ctx_lens.shape[0]
+    _ints("ctx_lens", ctx_lens, (R,))
+    _ints("new_lens", new_lens, (R,))
+    table, stride, width = _table(block_table, R)
+    _ints("free_blocks", free_blocks, (free_blocks.numel(),))
+    _ints("free_count", free_count, (1,))
+    given = [int(t.numel()) for t in (positions, slots) if t is not None]
+    T = int(num_tokens) if num_tokens is not None else (given[0] if given else None)
+    if T is None or any(n != T for n in given):
+        raise ValueError("num_tokens, or positions and slots of that length, must be given")
+    dev = ctx_lens.device
+    cu_seqlens = _empty((R + 1,), torch.int32, dev, stream) if cu_seqlens is None else _ints("cu_seqlens", cu_seqlens, (R + 1,))
+    seq_lens = _empty((R,), torch.int32, dev, stream) if seq_lens is None else _ints("seq_lens", seq_lens, (R,))
+    positions = _empty((T,), torch.int32, dev, stream) if positions is None else _ints("positions", positions, (T,))
+    slots = _empty((T,), torch.int64, dev, stream) if slots is None else _ints("slots", slots, (T,), torch.int64)
+    free_count_out = _empty((1,), torch.int32, dev, stream) if free_count_out is None else _ints("free_count_out", free_count_out, (1,))
+    _run("fa_kv_reserve", stream, ctx_lens.data_ptr(), new_lens.data_ptr(), R, table.data_ptr(), stride, width,
+         free_blocks.data_ptr(), free_count.data_ptr(), free_blocks.numel(), int(page_size), T, cu_seqlens.data_ptr(),
+         seq_lens.data_ptr(), positions.data_ptr(), slots.data_ptr(), free_count_out.data_ptr())
+    return cu_seqlens, seq_lens, positions, slots, free_count_out
+
+
+def fa_kv_release(lens, done, block_table, free_blocks, free_count, *, page_size: int, lens_out=None, free_count_out=None,
+                  stream=None):
+    """Gives the blocks of every request with done[r] != 0 back to the free stack (fa_kv_release);
+    returns (lens_out [R], free_count_out [1]).  lens_out may be lens, free_count_out free_count."""
+    import torch
+    R = lens.shape[0]
+    _ints("lens", lens, (R,))
+    _ints("done", done, (R,))
+    table, stride, width = _table(block_table, R)
+    _ints("free_blocks", free_blocks, (free_blocks.numel(),))
+    _ints("free_count", free_count, (1,))
+    dev = lens.device
+    lens_out = _empty((R,), torch.int32, dev, stream) if lens_out is None else _ints("lens_out", lens_out, (R,))
+    free_count_out = _empty((1,), torch.int32, dev, stream) if free_count_out is None else _ints("free_count_out", free_count_out, (1,))
+    _run("fa_kv_release", stream, lens.data_ptr(), done.data_ptr(), R, table.data_ptr(), stride, width, free_blocks.data_ptr(),
+         free_count.data_ptr(), free_blocks.numel(), int(page_size), lens_out.data_ptr(), free_count_out.data_ptr())
+    return lens_out, free_count_out
+
+
+def paged_workspace_bytes(Hq: int, Hkv: int, d: int) -> int:
+    return int(_core().lib().fa_paged_workspace_bytes(int(Hq), int(Hkv), int(d)))
+
+
+def fa_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, *, max_new: int, causal: bool = True,
+                 scale: float | None = None, window: int | None = None, out=None, lse=None, return_lse: bool = True,
+                 workspace=None, stream=None):
+    """Exact attention of new tokens over a paged cache (fa_paged_fwd): q [T, Hq, d] bf16 or fp16, request
+    r's tokens in rows cu_seqlens[r] .. cu_seqlens[r + 1] - 1 (at most max_new of them), its seq_lens[r]
+    keys (the new tokens' own among them) in the blocks block_table[r] of the caches, logically
+    [blocks, slots, Hkv, d].  Returns (out [T, Hq, d], lse [Hq, T] fp32 or None); rows of no request are
+    left as they are in `out` and `lse` (undefined in buffers made here)."""
+    import torch
+    f16 = _half(q)
+    qp, qs = _rows("q", q, q.dtype)
+    T, Hq, d = q.shape
+    c = _cache(k_cache, v_cache)
+    if k_cache.dtype != q.dtype or c.d != d:
+        raise ValueError(f"shape mismatch q{tuple(q.shape)} {q.dtype} cache{tuple(k_cache.shape)} {k_cache.dtype}")
+    R = seq_lens.shape[0]
+    _ints("seq_lens", seq_lens, (R,))
+    _ints("cu_seqlens", cu_seqlens, (R + 1,))
+    table, stride, width = _table(block_table, R)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = _empty((T, Hq, d), q.dtype, q.device, stream)
+    elif out.dtype != q.dtype or tuple(out.shape) != (T, Hq, d) or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous {q.dtype} {(T, Hq, d)}, got {out.dtype} {tuple(out.shape)}")
+    if not return_lse:
+        lse = None
+    elif lse is None:
+        lse = _empty((Hq, T), torch.float32, q.device, stream)
+    elif lse.dtype != torch.float32 or tuple(lse.shape) != (Hq, T) or not lse.is_contiguous():
+        raise ValueError(f"lse must be contiguous fp32 {(Hq, T)}, got {lse.dtype} {tuple(lse.shape)}")
+    if window is not None and int(window) < 1:
+        raise ValueError(f"window must be at least 1, got {window}")
+    if workspace is None:
+        workspace = _empty((max(1, paged_workspace_bytes(Hq, c.Hkv, d)),), torch.uint8, q.device, stream)
+    _run("fa_paged_fwd" + f16, stream, qp, qs, ctypes.byref(c), table.data_ptr(), stride, width, cu_seqlens.data_ptr(),
+         seq_lens.data_ptr(), R, T, Hq, int(max_new), float(scale), 1 if causal else 0, int(window) if window is not None else 0,
+         out.data_ptr(), lse.data_ptr() if lse is not None else None, workspace.data_ptr(),
+         workspace.numel() * workspace.element_size())
+    return out, lse
+
+
+class PagedKV:
+    """One layer's paged cache for up to `max_requests` requests, and a step over it: reserve() takes room
+    for the new tokens, append() rotates and stores them, attend() is the attention, release() gives the
+    blocks of finished requests back.  Everything is on the device; nothing synchronises.  With
+    several layers, one PagedKV holds the tables and the others are made with tables=that one.
+
+    layout "hnd" keeps a head's slots of a block together in memory, "nhd" a slot's heads."""
+
+    def __init__(self, max_requests: int, num_blocks: int, page_size: int, Hkv: int, d: int, *, max_blocks: int | None = None,
+                 dtype=None, device="cuda", layout: str = "nhd", tables: "PagedKV | None" = None):
+        import torch
+        if layout not in ("nhd", "hnd"):
+            raise ValueError(f"layout must be nhd or hnd, got {layout}")
+        dtype = dtype or torch.bfloat16
+        shape = (num_blocks, page_size, Hkv, d) if layout == "nhd" else (num_blocks, Hkv, page_size, d)
+        caches = [torch.zeros(shape, dtype=dtype, device=device) for _ in range(2)]
+        self.k_cache, self.v_cache = caches if layout == "nhd" else [c.permute(0, 2, 1, 3) for c in caches]
+        self.page_size, self.num_blocks, self.Hkv, self.d = page_size, num_blocks, Hkv, d
+        self.tables = tables or self
+        if tables is not None:
+            if (tables.page_size, tables.num_blocks) != (page_size, num_blocks) or tables.seq_lens.shape[0] != max_requests:
+                raise ValueError("layers that share tables have the same requests, blocks and page size")
+            return
+        ints = dict(dtype=torch.int32, device=device)
+        self.block_table = torch.zeros((max_requests, max_blocks or num_blocks), **ints)
+        self.seq_lens = torch.zeros(max_requests, **ints)
+        self.free_blocks = torch.arange(num_blocks - 1, -1, -1, **ints)
+        self.free_count = torch.full((1,), num_blocks, **ints)
+        self.cu_seqlens = torch.zeros(max_requests + 1, **ints)
+        self.positions = self.slots = None
+
+    def reserve(self, new_lens, num_tokens: int, *, stream=None):
+        """Room for new_lens [max_requests] int32 more tokens, num_tokens rows in all (rows behind the last
+        token are allowed: a captured step of fixed size).  Returns positions and slots."""
+        if self.tables is not self:
+            raise ValueError("reserve on the layer that holds the tables")
+        import torch
+        if self.slots is None or self.slots.numel() != num_tokens:
+            self.positions = _empty((num_tokens,), torch.int32, self.seq_lens.device, stream)
+            self.slots = _empty((num_tokens,), torch.int64, self.seq_lens.device, stream)
+        fa_kv_reserve(self.seq_lens, new_lens, self.block_table, self.free_blocks, self.free_count, page_size=self.page_size,
+                      cu_seqlens=self.cu_seqlens, seq_lens=self.seq_lens, positions=self.positions, slots=self.slots,
+                      free_count_out=self.free_count, stream=stream)
+        return self.positions, self.slots
+
+    def append(self, q, k, v, table: RopeTable, *, positions=None, q_out=None, stream=None):
+        """Rotates q and k by `positions` (default: the positions in the requests) and stores k and v."""
+        t = self.tables
+        if t.slots is None:
+            raise ValueError("reserve before append")
+        return fa_rope_append(q, k, v, t.positions if positions is None else positions, table, self.k_cache, self.v_cache, t.slots,
+                              q_out=q_out, stream=stream)
+
+    def attend(self, q, *, max_new: int, causal: bool = True, scale=None, window=None, out=None, lse=None, return_lse=True,
+               workspace=None, stream=None):
+        """Attention of the new tokens' (rotated) q [T, Hq, d]."""
+        t = self.tables
+        return fa_paged_fwd(q, self.k_cache, self.v_cache, t.block_table, t.cu_seqlens, t.seq_lens, max_new=max_new, causal=causal,
+                            scale=scale, window=window, out=out, lse=lse, return_lse=return_lse, workspace=workspace, stream=stream)
+
+    def release(self, done, *, stream=None):
+        """Gives back the blocks of every request with done[r] != 0 ([max_requests] int32)."""
+        if self.tables is not self:
+            raise ValueError("release on the layer that holds the tables")
+        fa_kv_release(self.seq_lens, done, self.block_table, self.free_blocks, self.free_count, page_size=self.page_size,
+                      lens_out=self.seq_lens, free_count_out=self.free_count, stream=stream)

@@ -61,8 +61,11 @@ enum fa_status_code {
     FA_ERR_NOT_DEVICE_MEMORY = 7,    /* a tensor pointer is not device memory of the current device,
                                         or its extent runs past the end of its allocation */
     FA_ERR_OVERLAP = 8,              /* out or lse overlaps an input or each other */
-    FA_ERR_SCRATCH_LIMIT = 9         /* fa_fwd_splitkv_static: the partials need more than the
+    FA_ERR_SCRATCH_LIMIT = 9,        /* fa_fwd_splitkv_static: the partials need more than the
                                         library's static scratch (FA_SPLITKV_STATIC_SCRATCH_BYTES) */
+    FA_ERR_PAGED_RANGE = 10          /* reported by fa_device_status: a length, block id, free count or
+                                        slot that a paged-cache kernel read on the device is out of
+                                        range; the entry point says what was left out */
 };
 
 /*
@@ -264,6 +267,145 @@ int fa_fwd_partial(const void *q, const void *k, const void *v, float *o_part, f
 int fa_merge_partials(const float *o_parts, const float *lse_parts, int R, void *out, float *lse,
                       int B, int Hq, int Nq, int d, void *stream);
 
+/*
+ * Paged key/value cache, for serving many requests whose lengths grow: keys and values live in
+ * blocks of page_size token slots, and a request's block table names the blocks that hold its
+ * tokens in order (position x of request r is slot x % page_size of block
+ * block_table[r][x / page_size]).  Free blocks are a stack: free_blocks[0 .. *free_count - 1].
+ * One step of a serving loop is fa_kv_reserve (room for the new tokens), fa_rope_append (their
+ * keys and values into the cache), fa_paged_fwd (attention); fa_kv_release gives the blocks of
+ * finished requests back.  Lengths, tables and counts stay on the device, so a step needs no
+ * host synchronisation and can be captured in a CUDA graph.
+ *
+ * fa_kv_reserve: request r holds ctx_lens[r] tokens and gets new_lens[r] more (0 allowed).
+ *     held_r = ceil(ctx_lens[r] / page_size), need_r = ceil((ctx + new) / page_size) - held_r;
+ *   block_table[r][held_r + n] (n < need_r) = the next free block, taken from the top of the
+ *   stack, requests in order: free_blocks[*free_count - 1 - (sum of need of the requests before + n)].
+ *   cu_seqlens [R + 1] = exclusive prefix sums of new_lens; seq_lens [R] = ctx_lens + new_lens;
+ *   positions [T] and slots [T] of the new tokens, request after request: the position in its
+ *   request and block * page_size + slot in the block; the rows behind the last token get
+ *   position 0 and slot -1.  *free_count_out = *free_count - sum of need.
+ *   block_table is [R, max_blocks], rows table_stride (>= max_blocks) entries apart; entries
+ *   that are not taken now are left as they are.  seq_lens may be ctx_lens and free_count_out
+ *   may be free_count (updated in place); otherwise no output may overlap an input or another
+ *   output.  A negative length, a request longer than max_blocks * page_size, more tokens than
+ *   T, or more blocks than are free: the whole step is refused on the device (FA_ERR_PAGED_RANGE
+ *   by fa_device_status; cu_seqlens all 0, seq_lens = ctx_lens, every slot -1, the table and
+ *   the free count unchanged).  A block id outside 0 .. num_blocks - 1, in the table or the free
+ *   stack, is reported the same way; tokens in such a block get slot -1.
+ * fa_kv_release: every request with done[r] != 0 gives back its ceil(lens[r] / page_size) blocks,
+ *   pushed on the free stack in table order, requests in order; lens_out[r] = 0 for those and
+ *   lens[r] for the others (lens_out may be lens, free_count_out may be free_count).  The table
+ *   is not changed.  Lengths out of range, or more blocks than num_blocks in the stack: refused
+ *   whole, as above.
+ * R, T, max_blocks, num_blocks >= 0, page_size >= 1, max_blocks * page_size < 2^31.  int32 arrays
+ * 4-byte aligned, slots 8-byte; empty arrays may be NULL.
+ */
+int fa_kv_reserve(const int *ctx_lens, const int *new_lens, int R, int *block_table, long long table_stride,
+                  int max_blocks, const int *free_blocks, const int *free_count, int num_blocks, int page_size,
+                  int T, int *cu_seqlens, int *seq_lens, int *positions, long long *slots, int *free_count_out,
+                  void *stream);
+int fa_kv_release(const int *lens, const int *done, int R, const int *block_table, long long table_stride,
+                  int max_blocks, int *free_blocks, const int *free_count, int num_blocks, int page_size,
+                  int *lens_out, int *free_count_out, void *stream);
+
+/*
+ * The keys and values of a paged cache: element e of head h of slot s of block b is
+ * k[b * block_stride + s * slot_stride + h * head_stride + e] (strides in elements, multiples of
+ * 8; 16-byte aligned bases; v likewise), so a block may keep its slots together per head
+ * ([block, head, slot, d]) or its heads together per slot ([block, slot, head, d]).  No two
+ * (b, s, h) may share memory: each of the three strides is >= the extent of the ones inside it.
+ */
+typedef struct fa_paged_cache {
+    void *k, *v;                                      /* bf16 or fp16, device memory */
+    long long block_stride, slot_stride, head_stride; /* elements */
+    int num_blocks, page_size, Hkv, d;
+} fa_paged_cache;
+
+/*
+ * Rotary position embedding with several position axes (time, height, width, ...).  Pair i of a
+ * head (i < rot_dim / 2) turns by angle = positions[axis[i]][t] * inv_freq[i]:
+ *     (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin),
+ * where (x1, x2) are the elements (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved; elements
+ * from rot_dim on are copied.  The spec is host memory, read during the call.
+ */
+typedef struct fa_rope_spec {
+    int rot_dim;             /* even, 0 .. d */
+    int interleaved;         /* 0 or 1 */
+    int num_axes;            /* 1 .. 4 */
+    const double *inv_freq;  /* [rot_dim / 2], finite */
+    const int *axis;         /* [rot_dim / 2], each 0 .. num_axes - 1; NULL: all 0 */
+} fa_rope_spec;
+
+/*
+ * fa_rope: q [T, Hq, d] -> q_out and k [T, Hkv, d] -> k_out, bf16 (fa_rope_f16: fp16), rows
+ *   *_stride (>= heads * d) elements from token to token, so q, k may be slices of one fused
+ *   projection; positions [num_axes, T] int32, axes pos_stride (>= T) apart.  inverse = 1 turns
+ *   by the opposite angle: the gradient of the forward turn (dq, dk of the rotated rows -> of
+ *   the rows).  Angles are formed in fp64 and applied in fp32, one rounding at the end.  Hq or
+ *   Hkv may be 0.  In place (q_out == q with the same stride, k_out == k) is allowed; otherwise
+ *   no output row may overlap an input row or another output row.
+ * fa_rope_append: q as above (forward turn; q_out NULL with Hq = 0), and for each token t with
+ *   slots[t] >= 0 the rotated k row and the v row go to slot slots[t] % page_size of block
+ *   slots[t] / page_size of the cache.  Rows with a negative slot are left out: neither read
+ *   nor written, q_out included.  A slot >= num_blocks * page_size is left out too and reported
+ *   (FA_ERR_PAGED_RANGE).  Two rows with the same slot: one of them is kept, which is not defined.
+ * d as fa_fwd.  Rows that are 16-byte aligned (base and stride) with rot_dim a multiple of 16
+ * take the vector path; any others work, slower.
+ */
+int fa_rope(const void *q, long long q_stride, void *q_out, long long qo_stride, int Hq, const void *k,
+            long long k_stride, void *k_out, long long ko_stride, int Hkv, int T, int d, const int *positions,
+            long long pos_stride, const fa_rope_spec *spec, int inverse, void *stream);
+int fa_rope_f16(const void *q, long long q_stride, void *q_out, long long qo_stride, int Hq, const void *k,
+                long long k_stride, void *k_out, long long ko_stride, int Hkv, int T, int d, const int *positions,
+                long long pos_stride, const fa_rope_spec *spec, int inverse, void *stream);
+int fa_rope_append(const void *q, long long q_stride, void *q_out, long long qo_stride, int Hq, const void *k,
+                   long long k_stride, const void *v, long long v_stride, int T, const int *positions,
+                   long long pos_stride, const fa_rope_spec *spec, const fa_paged_cache *cache,
+                   const long long *slots, void *stream);
+int fa_rope_append_f16(const void *q, long long q_stride, void *q_out, long long qo_stride, int Hq, const void *k,
+                       long long k_stride, const void *v, long long v_stride, int T, const int *positions,
+                       long long pos_stride, const fa_rope_spec *spec, const fa_paged_cache *cache,
+                       const long long *slots, void *stream);
+
+/*
+ * fa_paged_fwd -- exact attention of new tokens over a paged cache (fa_paged_fwd_f16: fp16).
+ *
+ *   q   [T, Hq, d], rows q_stride (>= Hq * d, a multiple of 8) elements apart, 16-byte aligned:
+ *       request r's new tokens are rows cu_seqlens[r] .. cu_seqlens[r + 1] - 1 (n_r of them)
+ *   cache: keys and values (Hkv heads, Hq % Hkv == 0; query head h reads head h / (Hq / Hkv))
+ *   block_table [R, max_blocks] (rows table_stride apart), cu_seqlens [R + 1], seq_lens [R]:
+ *       int32 device arrays; seq_lens[r] = L_r keys in all, the new tokens' own among them
+ *   out [T, Hq, d] dense, 16-byte aligned;  lse [Hq, T] fp32 natural log, or NULL
+ *   max_new: an upper bound of n_r, known on the host
+ *
+ * New token i of request r sees key j < L_r iff (causal = 0 or j <= i + L_r - n_r) and
+ * (window = 0 or j > i + L_r - n_r - window); window > 0 needs causal = 1.  A row that sees no
+ * key gets O = 0 and LSE = -inf.  Rows of out and lse outside every request are left as they are.
+ * Only blocks that hold a visible key are looked up and read; slots of such a block behind L_r may hold
+ * anything, NaN included.
+ *
+ * workspace: caller-owned device scratch, 256-byte aligned, of at least
+ *   fa_paged_workspace_bytes(Hq, Hkv, d) bytes (independent of R, T and the lengths; 0 for invalid
+ *   sizes).  No initial contents are needed; two calls must not share one concurrently.
+ * The work is split evenly over the GPU at any mix of lengths (one long request included), and
+ * the partial results of a split (request, head) are merged in a fixed order: the same inputs
+ * give the same bits.
+ * A request with seq_lens < 0 or > max_blocks * page_size, cu_seqlens not ascending within
+ * 0 .. T, or n_r > max_new is left out (its rows unchanged), and a block id outside
+ * 0 .. num_blocks - 1 where a visible key is reads as zeros; both are reported
+ * (FA_ERR_PAGED_RANGE by fa_device_status).
+ */
+size_t fa_paged_workspace_bytes(int Hq, int Hkv, int d);
+int fa_paged_fwd(const void *q, long long q_stride, const fa_paged_cache *cache, const int *block_table,
+                 long long table_stride, int max_blocks, const int *cu_seqlens, const int *seq_lens, int R, int T,
+                 int Hq, int max_new, float scale, int causal, int window, void *out, float *lse, void *workspace,
+                 size_t workspace_bytes, void *stream);
+int fa_paged_fwd_f16(const void *q, long long q_stride, const fa_paged_cache *cache, const int *block_table,
+                     long long table_stride, int max_blocks, const int *cu_seqlens, const int *seq_lens, int R,
+                     int T, int Hq, int max_new, float scale, int causal, int window, void *out, float *lse,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
 /* Human-readable text of a status code (static storage; never NULL). */
 /*
  * fa_test_withheld_load -- the failure path of the forward kernel, for tests (no counterpart
@@ -286,10 +428,12 @@ const char *fa_status_string(int status);
 
 /*
  * fa_device_status -- synchronises `stream`, then returns and clears the current
- * device's kernel status word: FA_OK, or FA_ERR_DEVICE_TIMEOUT if a pipeline wait in a
- * forward or backward kernel ran out of time.  FA_ERR_CUDA if the synchronisation itself
- * failed.  If `detail` is not NULL it receives the raw status word (bits 8..15 name the
- * wait: 1-12 forward, 21-34 backward; bits 16.. the CTA).
+ * device's kernel status word: FA_OK, FA_ERR_DEVICE_TIMEOUT if a pipeline wait in a
+ * forward or backward kernel ran out of time, or FA_ERR_PAGED_RANGE (the first report is
+ * kept).  FA_ERR_CUDA if the synchronisation itself failed.  If `detail` is not NULL it
+ * receives the raw status word (bits 8..15 name the wait: 1-12 forward, 21-34 backward; bits
+ * 16.. the CTA; for FA_ERR_PAGED_RANGE bits 8..15: 41 lengths, 42 tokens, 43 free blocks, 44 a
+ * free-stack entry, 45 a table entry, 46 a slot; bits 16.. the request, or the token of a slot).
  */
 int fa_device_status(void *stream, int *detail);
 

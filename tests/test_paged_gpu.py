@@ -1,0 +1,537 @@
+"""The paged-cache operators on the GPU against plain 64-bit references: block tables and slots, rotary
+embedding, attention over the cache, and a serving loop that runs them together."""
+import math
+import random
+
+import pytest
+
+import exact_attention_146_b200 as fa
+from tests import _paged
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built_library():
+    from exact_attention_146_b200 import build
+    build.build()
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    fa.device_status()
+    yield
+
+
+@pytest.fixture(autouse=True)
+def status_is_clean():
+    yield
+    st, word = fa.device_status()
+    assert st == fa.FA_OK, f"device status {st} ({word:#x})"
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------------------- block tables
+
+def pool(ctx, page, max_blocks, spare, seed):
+    """A table of the requests' blocks and a stack of `spare` free ones."""
+    rng = random.Random(seed)
+    held = [_paged.blocks_of(c, page) for c in ctx]
+    ids = list(range(sum(held) + spare))
+    rng.shuffle(ids)
+    table, at = [], 0
+    for n in held:
+        table.append(ids[at:at + n] + [-7] * (max_blocks - n))
+        at += n
+    return table, ids[at:] + [-9] * at, spare
+
+
+@pytest.mark.parametrize("R,page,most,pad,stride", [(1, 16, 1, 0, 0), (1, 1, 5, 2, 0), (7, 16, 40, 3, 5), (33, 48, 300, 0, 0),
+                                                    (256, 16, 1, 5, 0), (257, 5, 9, 0, 1), (1024, 16, 3, 1, 0),
+                                                    (1025, 32, 2, 0, 0), (2600, 16, 100, 17, 0), (3, 128, 4096, 0, 0)])
+def test_reserve_then_release(R, page, most, pad, stride):
+    rng = random.Random(R * 31 + page)
+    ctx = [rng.choice([0, 1, page - 1, page, page + 1, rng.randint(0, 5 * page)]) for _ in range(R)]
+    new = [rng.choice([0, 1, most, rng.randint(0, most)]) for _ in range(R)]
+    width = max(_paged.blocks_of(c + n, page) for c, n in zip(ctx, new)) + 1
+    spare = sum(_paged.blocks_of(c + n, page) - _paged.blocks_of(c, page) for c, n in zip(ctx, new)) + 2
+    table, free, count = pool(ctx, page, width, spare, R)
+    T = sum(new) + pad
+    whole = i32([row + [-5] * stride for row in table])
+    tab = whole[:, :width]
+    cu, lens, pos, slots, cnt = fa.fa_kv_reserve(i32(ctx), i32(new), tab, i32(free), i32([count]), page_size=page, num_tokens=T)
+    ref = _paged.reserve_plain(ctx, new, table, free, count, page, T, width)
+    assert cu.tolist() == ref[0] and lens.tolist() == ref[1] and pos.tolist() == ref[2] and slots.tolist() == ref[3]
+    assert cnt.tolist() == [ref[4]] and tab.tolist() == ref[5]
+    assert stride == 0 or bool((whole[:, width:] == -5).all())
+    # in place, and back
+    ctx_d, cnt_d, tab2 = i32(ctx), i32([count]), i32(table)
+    fa.fa_kv_reserve(ctx_d, i32(new), tab2, i32(free), cnt_d, page_size=page, num_tokens=T, seq_lens=ctx_d, free_count_out=cnt_d)
+    assert ctx_d.tolist() == ref[1] and cnt_d.tolist() == [ref[4]] and tab2.tolist() == ref[5]
+    done = [rng.choice([0, 0, 1, 5]) for _ in range(R)]
+    stack = i32(free)
+    fa.fa_kv_release(ctx_d, i32(done), tab2, stack, cnt_d, page_size=page, lens_out=ctx_d, free_count_out=cnt_d)
+    want, n = list(free), ref[4]
+    for r in range(R):
+        if done[r]:
+            for b in range(_paged.blocks_of(ref[1][r], page)):
+                want[n] = ref[5][r][b]
+                n += 1
+    assert cnt_d.tolist() == [n] and stack.tolist() == want and tab2.tolist() == ref[5]
+    assert ctx_d.tolist() == [0 if f else x for f, x in zip(done, ref[1])]
+
+
+def test_reserve_of_no_requests():
+    cu, lens, pos, slots, cnt = fa.fa_kv_reserve(i32([]), i32([]), torch.zeros((0, 4), dtype=torch.int32, device="cuda"), i32([3, 4]),
+                                                 i32([2]), page_size=16, num_tokens=5)
+    assert cu.tolist() == [0] and slots.tolist() == [-1] * 5 and pos.tolist() == [0] * 5 and cnt.tolist() == [2]
+
+
+@pytest.mark.parametrize("ctx,new,free,count,site", [
+    ([3, -1], [1, 1], [0, 1, 2, 3, 4, 5], 6, 41),          # a negative length
+    ([3, 20], [1, -2], [0, 1, 2, 3, 4, 5], 6, 41),
+    ([3, 60], [1, 10], [0, 1, 2, 3, 4, 5], 6, 41),         # longer than its row of the table (4 x 16)
+    ([3, 20], [5, 10], [0, 1, 2, 3, 4, 5], 6, 42),         # more tokens than rows
+    ([0, 0], [4, 4], [0, 1, 2, 3, 4, 5], 1, 43),           # more blocks than are free
+    ([0, 0], [4, 4], [0, 1, 2, 3, 4, 5], 9, 43),           # a count beyond the stack
+])
+def test_reserve_refuses_a_whole_step(ctx, new, free, count, site):
+    table = i32([[7, 7, 7, 7]] * 2)
+    cu, lens, pos, slots, cnt = fa.fa_kv_reserve(i32(ctx), i32(new), table, i32(free), i32([count]), page_size=16, num_tokens=12)
+    st, word = fa.device_status()
+    assert st == fa.FA_ERR_PAGED_RANGE and (word >> 8) & 0xFF == site
+    assert cu.tolist() == [0, 0, 0] and lens.tolist() == ctx and slots.tolist() == [-1] * 12 and cnt.tolist() == [count]
+    assert bool((table == 7).all())
+
+
+def test_bad_block_ids_are_reported_and_get_no_slot():
+    table = i32([[99, -1], [3, -1]])
+    _, _, pos, slots, _ = fa.fa_kv_reserve(i32([3, 15]), i32([2, 3]), table, i32([0, -4]), i32([2]), page_size=16, num_tokens=5)
+    st, word = fa.device_status()
+    assert st == fa.FA_ERR_PAGED_RANGE and (word >> 8) & 0xFF in (44, 45)
+    assert pos.tolist() == [3, 4, 15, 16, 17] and slots.tolist() == [-1, -1, -1, -1, -1]   # 2 blocks: ids 0 and 1 alone are right
+
+
+def test_release_refuses_more_blocks_than_the_stack_holds():
+    stack = i32([5, 6, 7, 8])
+    lens, cnt = fa.fa_kv_release(i32([33, 4]), i32([1, 0]), i32([[0, 1, 2], [3, 0, 0]]), stack, i32([2]), page_size=16)
+    st, word = fa.device_status()
+    assert st == fa.FA_ERR_PAGED_RANGE and (word >> 8) & 0xFF == 43
+    assert lens.tolist() == [33, 4] and cnt.tolist() == [2] and stack.tolist() == [5, 6, 7, 8]
+
+
+# ------------------------------------------------------------------------------- rotary embedding
+
+def spec(rot, axes):
+    inv = [10000.0 ** (-2.0 * i / max(rot, 1)) for i in range(rot // 2)]
+    return inv, [i % axes for i in range(rot // 2)]
+
+
+ROPE = [(torch.bfloat16, 128, 128, 1, False, 1, 4, 2), (torch.float16, 128, 64, 2, True, 700, 3, 1),
+        (torch.bfloat16, 80, 80, 3, False, 33, 16, 16), (torch.bfloat16, 80, 20, 3, True, 129, 5, 1),
+        (torch.float16, 32, 32, 4, False, 1000, 1, 1), (torch.bfloat16, 64, 6, 1, False, 3, 2, 2),
+        (torch.float16, 256, 256, 1, True, 601, 8, 1), (torch.bfloat16, 192, 96, 3, False, 64, 6, 2),
+        (torch.bfloat16, 96, 0, 1, False, 5, 2, 1), (torch.float16, 96, 96, 1, True, 2500, 2, 0)]
+
+
+def close(got, want, tol):
+    bad = (got.double() - want).abs() > tol
+    assert not bool(bad.any()), f"{int(bad.sum())} of {bad.numel()} off, worst {float(((got.double() - want).abs() / tol).max()):.2f} of the tolerance"
+
+
+@pytest.mark.parametrize("dtype,d,rot,axes,pairs,T,Hq,Hkv", ROPE)
+def test_rope_and_its_gradient(dtype, d, rot, axes, pairs, T, Hq, Hkv):
+    torch.manual_seed(T + d)
+    inv, axis = spec(rot, axes)
+    table = fa.RopeTable(inv, axis=axis, interleaved=pairs)
+    fused = torch.randn(T, Hq + 2 * Hkv, d, device="cuda").to(dtype)
+    q, k = fused[:, :Hq], (fused[:, Hq:Hq + Hkv] if Hkv else None)
+    pos = torch.randint(0, 1 << 20, (axes, T), device="cuda", dtype=torch.int32)
+    for inverse in (False, True):
+        got = fa.fa_rope(q, pos, table, k=k, inverse=inverse)
+        got = got if Hkv else (got,)
+        for g, x in zip(got, (q, k)):
+            want = _paged.rope64(x, pos, inv, axis, pairs, -1.0 if inverse else 1.0)
+            close(g, want, _paged.rope_tolerance(x, want, rot // 2, pairs))
+    # in place on the projection: the same bits; what lies between the rows stays
+    again = fused.clone()
+    fa.fa_rope(again[:, :Hq], pos, table, k=again[:, Hq:Hq + Hkv] if Hkv else None, q_out=again[:, :Hq],
+               k_out=again[:, Hq:Hq + Hkv] if Hkv else None)
+    fresh = fa.fa_rope(q, pos, table, k=k)
+    fresh = fresh if Hkv else (fresh,)
+    assert torch.equal(again[:, :Hq], fresh[0]) and (Hkv == 0 or torch.equal(again[:, Hq:Hq + Hkv], fresh[1]))
+    assert torch.equal(again[:, Hq + Hkv:], fused[:, Hq + Hkv:])
+
+
+def test_rope_gradient_against_differences():
+    """f(x) = sum(g * rope(x)) is linear: (f(x + h e) - f(x - h e)) / 2h in 64 bits is the gradient."""
+    torch.manual_seed(5)
+    inv, axis = spec(16, 2)
+    pos = torch.randint(0, 5000, (2, 3), device="cuda", dtype=torch.int32)
+    for pairs in (False, True):
+        x = torch.randn(3, 1, 32, device="cuda").to(torch.float16)
+        g = torch.randn(3, 1, 32, device="cuda").to(torch.float16)
+        got = fa.fa_rope(g, pos, fa.RopeTable(inv, axis=axis, interleaved=pairs), inverse=True)
+
+        def f(y):
+            return float((_paged.rope64(y, pos, inv, axis, pairs) * g.double()).sum())
+        for t in range(3):
+            for e in range(32):
+                h = torch.zeros(3, 1, 32, dtype=torch.float64, device="cuda")
+                h[t, 0, e] = 0.5
+                diff = f(x.double() + h) - f(x.double() - h)
+                size = float(g[t].double().abs().max())
+                assert abs(float(got[t, 0, e]) - diff) <= 2.0 ** -11 * abs(diff) + 2.0 ** -19 * size + 2.0 ** -25
+
+
+@pytest.mark.parametrize("shift", [0, 1, 3])
+def test_rope_of_unaligned_rows(shift):
+    """Rows that start off a 16-byte boundary take the path of single values: the same numbers."""
+    torch.manual_seed(9)
+    inv, axis = spec(64, 1)
+    table = fa.RopeTable(inv, axis=axis)
+    buf = torch.randn(9 * (3 * 64 + shift) + 8, device="cuda").to(torch.bfloat16)
+    x = torch.as_strided(buf, (9, 3, 64), (3 * 64 + shift, 64, 1), shift)
+    pos = torch.arange(9, device="cuda", dtype=torch.int32) * 1000
+    want = _paged.rope64(x, pos[None], inv, axis, False)
+    close(fa.fa_rope(x, pos, table), want, _paged.rope_tolerance(x, want, 32, False))
+
+
+@pytest.mark.parametrize("dtype,d,rot,axes,pairs,T,Hq,Hkv", ROPE[:9])
+@pytest.mark.parametrize("layout", ["nhd", "hnd", "pair"])
+def test_rope_append(dtype, d, rot, axes, pairs, T, Hq, Hkv, layout):
+    torch.manual_seed(T + d + 1)
+    inv, axis = spec(rot, axes)
+    page = 16
+    k_cache, v_cache, _ = _paged.make_paged([T], page, Hkv, d, dtype, layout, 3, poison=False)
+    before = k_cache.clone(), v_cache.clone()
+    fused = torch.randn(T, Hq + 2 * Hkv, d, device="cuda").to(dtype)
+    q, k, v = fused[:, :Hq], fused[:, Hq:Hq + Hkv], fused[:, Hq + Hkv:]
+    pos = torch.randint(0, 1 << 17, (axes, T), device="cuda", dtype=torch.int32)
+    slots = torch.randperm(k_cache.shape[0] * page, device="cuda")[:T]
+    slots[torch.rand(T, device="cuda") < 0.2] = -1
+    q_out = torch.full((T, Hq, d), 7.0, device="cuda", dtype=dtype)
+    fa.fa_rope_append(q, k, v, pos, fa.RopeTable(inv, axis=axis, interleaved=pairs), k_cache, v_cache, slots, q_out=q_out)
+    real = slots >= 0
+    assert bool((q_out[~real] == 7.0).all())
+    want = _paged.rope64(q, pos, inv, axis, pairs)
+    close(q_out[real], want[real], _paged.rope_tolerance(q, want, rot // 2, pairs)[real])
+    at = slots[real] // page, slots[real] % page
+    want = _paged.rope64(k, pos, inv, axis, pairs)
+    close(k_cache[at], want[real], _paged.rope_tolerance(k, want, rot // 2, pairs)[real])
+    assert torch.equal(v_cache[at], v[real])
+    rest = torch.ones(k_cache.shape[:2], dtype=torch.bool, device="cuda")
+    rest[at] = False
+    assert torch.equal(k_cache[rest], before[0][rest]) and torch.equal(v_cache[rest], before[1][rest])
+
+
+def test_rope_append_reports_a_slot_past_the_cache():
+    k_cache, v_cache, _ = _paged.make_paged([16], 16, 1, 64, torch.bfloat16, "nhd", 4, poison=False)
+    x = torch.randn(3, 1, 64, device="cuda").to(torch.bfloat16)
+    slots = torch.tensor([0, 64 * 16, 1], device="cuda")
+    fa.fa_rope_append(None, x, x, i32([0, 1, 2]), fa.RopeTable([1.0] * 32), k_cache, v_cache, slots)
+    st, word = fa.device_status()
+    assert st == fa.FA_ERR_PAGED_RANGE and (word >> 8) & 0xFF == 46 and word >> 16 == 1
+    assert torch.equal(v_cache[0, 0], x[0]) and torch.equal(v_cache[0, 1], x[2])
+
+
+# ------------------------------------------------------------------------------- attention over the cache
+
+def attend(lens, news, *, Hq, Hkv, d, page, dtype=torch.bfloat16, layout="nhd", causal=True, window=None, scale=None, pad=0, seed=0,
+           gap=0, max_new=None, workspace=None, sharp=1.0, poison=True):
+    """Runs fa_paged_fwd and compares every row; rows of no request keep their canary."""
+    k, v, table = _paged.make_paged(lens, page, Hkv, d, dtype, layout, seed + 1, poison=poison)
+    T = sum(news) + pad
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    q = (torch.empty(T, Hq + gap, d, device="cuda").normal_(generator=g) * sharp).to(dtype)[:, :Hq]
+    cu = [0]
+    for n in news:
+        cu.append(cu[-1] + n)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    out = torch.full((T, Hq, d), 3.0, device="cuda", dtype=dtype)
+    lse = torch.full((Hq, T), 3.0, device="cuda")
+    kw = dict(max_new=max(news, default=0) if max_new is None else max_new, causal=causal, window=window, scale=scale, workspace=workspace)
+    fa.fa_paged_fwd(q, k, v, table, i32(cu), i32(lens), out=out, lse=lse, **kw)
+    st, word = fa.device_status()
+    assert st == fa.FA_OK, f"device status {st} ({word:#x})"
+    want, z, t_out, t_lse = _paged.attend64(q, k, v, table, cu, lens, causal=causal, window=window, scale=scale)
+    n = sum(news)
+    close(out[:n], want[:n], t_out[:n])
+    none = torch.isinf(z[:, :n])
+    assert torch.equal(torch.isinf(lse[:, :n]), none) and bool((lse[:, :n][none] < 0).all())
+    close(torch.where(none, 0.0, lse[:, :n]), torch.where(none, 0.0, z[:, :n]), t_lse[:, :n])
+    assert bool((out[n:] == 3.0).all()) and bool((lse[:, n:] == 3.0).all())
+    again = torch.full_like(out, 3.0)
+    fa.fa_paged_fwd(q, k, v, table, i32(cu), i32(lens), out=again, return_lse=False, **kw)
+    assert torch.equal(out, again)   # the same bits, with or without the LSE
+    return q, k, v, table, cu, out, lse
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [32, 64, 80, 96, 128, 192, 256])
+def test_decode_every_head_dim(d, dtype):
+    attend([1, 16, 17, 300, 1037, 0, 129], [1, 1, 1, 1, 1, 0, 1], Hq=8, Hkv=2, d=d, page=16, dtype=dtype, pad=3, seed=d)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 1), (8, 8), (6, 2), (16, 1), (32, 1), (10, 2), (24, 2), (40, 2), (14, 2)])
+def test_decode_head_ratios(Hq, Hkv):
+    attend([33, 250, 1, 77], [1, 1, 1, 1], Hq=Hq, Hkv=Hkv, d=64, page=32, seed=Hq)
+
+
+@pytest.mark.parametrize("page", [1, 3, 8, 16, 24, 48, 100, 256])
+@pytest.mark.parametrize("layout", ["nhd", "hnd", "pair"])
+def test_pages_and_layouts(page, layout):
+    attend([130, 1, 513, 255], [1, 1, 1, 0], Hq=4, Hkv=2, d=64, page=page, layout=layout, seed=page)
+    attend([130, 40, 513, 255], [100, 1, 30, 0], Hq=4, Hkv=2, d=64, page=page, layout=layout, seed=page + 1)
+
+
+@pytest.mark.parametrize("new", [2, 3, 4, 7, 8, 16, 17, 31])
+def test_a_few_new_tokens(new):
+    attend([new, 500, 129, 64 + new], [new, new, 1, new // 2], Hq=8, Hkv=2, d=128, page=16, seed=new)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [32, 64, 80, 96, 128, 192, 256])
+def test_chunks_every_head_dim(d, dtype):
+    attend([700, 1, 333, 0, 900, 257], [300, 1, 333, 0, 65, 256], Hq=4, Hkv=2, d=d, page=16, dtype=dtype, pad=5, seed=d, gap=2)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(2, 2), (3, 1), (12, 4), (16, 1), (5, 1), (40, 1), (14, 2), (130, 1)])
+def test_chunks_head_ratios(Hq, Hkv):
+    attend([400, 90, 129], [150, 33, 1], Hq=Hq, Hkv=Hkv, d=64, page=16, seed=Hq)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("window", [1, 5, 16, 100, 128, 129, 5000])
+def test_window(window, d):
+    attend([1000, 40, 129, 2000], [260, 40, 1, 1], Hq=4, Hkv=2, d=d, page=16, window=window, seed=window)
+    attend([1000, 40, 129, 2000], [1, 1, 1, 2], Hq=4, Hkv=2, d=d, page=16, window=window, seed=window)
+
+
+@pytest.mark.parametrize("d", [80, 128, 256])
+def test_no_mask(d):
+    attend([1000, 40, 129], [260, 50, 1], Hq=4, Hkv=2, d=d, page=32, causal=False, seed=d)
+    attend([1000, 40, 129], [1, 2, 1], Hq=4, Hkv=2, d=d, page=32, causal=False, seed=d)
+
+
+@pytest.mark.parametrize("news,lens", [([5, 3], [3, 0]), ([300, 200], [40, 0]), ([1, 1], [0, 0]), ([140], [1])])
+def test_rows_that_see_no_key(news, lens):
+    """More new tokens than keys: the first rows see nothing (O = 0, LSE = -inf)."""
+    attend(lens, news, Hq=4, Hkv=2, d=64, page=16, seed=7)
+    attend(lens, news, Hq=4, Hkv=2, d=128, page=16, causal=False, seed=8)
+
+
+@pytest.mark.parametrize("new", [1, 130])
+def test_large_scores(new):
+    """Scores of a few hundred: the running maximum moves and the old sums are rescaled."""
+    attend([1500, 640], [new, 1], Hq=4, Hkv=1, d=128, page=16, sharp=25.0, seed=new)
+
+
+@pytest.mark.parametrize("new,L", [(1, 40000), (200, 30000), (2000, 2000)])
+def test_one_long_request(new, L):
+    attend([L], [new], Hq=8, Hkv=1, d=128, page=64, layout="hnd", seed=L)
+
+
+def test_many_requests():
+    rng = random.Random(3)
+    lens = [rng.randint(1, 60) for _ in range(1100)]
+    attend(lens, [rng.choice([0, 1, 1]) for _ in lens], Hq=2, Hkv=1, d=64, page=16, seed=3)
+    attend(lens[:300], [rng.randint(0, n) for n in lens[:300]], Hq=2, Hkv=1, d=64, page=16, seed=4)
+
+
+def test_max_new_is_only_a_bound():
+    for bound in (1, 4, 5, 70, 1000):
+        attend([300, 41], [1, 1], Hq=8, Hkv=2, d=128, page=16, max_new=bound, seed=1)
+
+
+def test_workspace_holds_anything():
+    """No initial contents are needed, and the size given by the library is enough: a canary behind it stays."""
+    need = fa.paged_workspace_bytes(8, 2, 128)
+    buf = torch.full((need + 4096,), 255, dtype=torch.uint8, device="cuda")   # NaN everywhere
+    for news in ([1, 1, 1], [700, 1, 90]):
+        attend([5000, 41, 800], news, Hq=8, Hkv=2, d=128, page=16, workspace=buf[:need], seed=2)
+        assert bool((buf[need:] == 255).all())
+
+
+@pytest.mark.parametrize("news,max_new,lens,cu,site", [
+    ([1, 1], 1, [20, -1], None, 41), ([1, 1], 1, [20, 5000], None, 41), ([3, 1], 2, [20, 9], None, 41),
+    ([200, 1], 200, [220, -5], None, 41), ([1, 1], 1, [20, 9], [0, 1, 99], 41), ([1, 1], 1, [20, 9], [1, 0, 1], 41)])
+def test_requests_out_of_range_are_left_out(news, max_new, lens, cu, site):
+    """The others are right, the left out one's rows stay as they were, and the status word tells."""
+    good = [n if 0 <= n <= 300 else 9 for n in lens]
+    k, v, table = _paged.make_paged(good, 16, 1, 64, torch.bfloat16, "nhd", 1)
+    T = sum(news)
+    q = torch.randn(T, 2, 64, device="cuda").to(torch.bfloat16)
+    at = cu or [0, news[0], T]
+    out, lse = torch.full((T, 2, 64), 3.0, device="cuda", dtype=q.dtype), torch.full((2, T), 3.0, device="cuda")
+    fa.fa_paged_fwd(q, k, v, table, i32(at), i32(lens), max_new=max_new, out=out, lse=lse)
+    st, word = fa.device_status()
+    assert st == fa.FA_ERR_PAGED_RANGE and (word >> 8) & 0xFF == site
+    width = table.shape[1] * 16
+    for r in range(2):
+        lo, hi = at[r], at[r + 1]
+        if not (0 <= lo <= hi <= T):
+            continue
+        if hi - lo > max_new or not 0 <= lens[r] <= width:
+            assert bool((out[lo:hi] == 3.0).all()) and bool((lse[:, lo:hi] == 3.0).all())
+        else:
+            want, z, t_out, t_lse = _paged.attend64(q, k, v, table, [0] * r + [lo, hi], [0] * r + [lens[r]], causal=True, window=None,
+                                                    scale=0.125)
+            close(out[lo:hi], want[lo:hi], t_out[lo:hi])
+
+
+@pytest.mark.parametrize("new", [1, 100])
+def test_a_block_that_does_not_exist_reads_as_zeros(new):
+    lens = [200]
+    k, v, table = _paged.make_paged(lens, 16, 2, 64, torch.bfloat16, "nhd", 1)
+    q = torch.randn(new, 4, 64, device="cuda").to(torch.bfloat16)
+    bad = table.clone()
+    bad[0, 3], bad[0, 7] = -1, k.shape[0]
+    out, _ = fa.fa_paged_fwd(q, k, v, bad, i32([0, new]), i32(lens), max_new=new)
+    st, word = fa.device_status()
+    assert st == fa.FA_ERR_PAGED_RANGE and (word >> 8) & 0xFF == 45
+    for b in (3, 7):
+        k[table[0, b].item()], v[table[0, b].item()] = 0.0, 0.0
+    want, _, t_out, _ = _paged.attend64(q, k, v, table, [0, new], lens, causal=True, window=None, scale=0.125)
+    close(out, want, t_out)
+
+
+def test_pages_outside_the_window_are_not_looked_up():
+    """A serving loop may have given back the blocks that its window has left."""
+    for new in (1, 90):
+        lens = [1000]
+        k, v, table = _paged.make_paged(lens, 16, 1, 64, torch.bfloat16, "nhd", 1)
+        first = 1000 - new - 64 + 1
+        gone = first // 16
+        q = torch.randn(new, 2, 64, device="cuda").to(torch.bfloat16)
+        want, _, t_out, _ = _paged.attend64(q, k, v, table, [0, new], lens, causal=True, window=64, scale=0.125)
+        for b in range(gone):
+            k[table[0, b].item()] = v[table[0, b].item()] = float("nan")
+        table[0, :gone] = -1
+        out, _ = fa.fa_paged_fwd(q, k, v, table, i32([0, new]), i32(lens), max_new=new, window=64)
+        close(out, want, t_out)
+
+
+@pytest.mark.parametrize("new", [1, 120])
+def test_on_a_stream_of_its_own(new):
+    s = torch.cuda.Stream()
+    k, v, table = _paged.make_paged([400], 16, 1, 64, torch.bfloat16, "nhd", 1)
+    q = torch.randn(new, 2, 64, device="cuda").to(torch.bfloat16)
+    torch.cuda.synchronize()
+    out, lse = fa.fa_paged_fwd(q, k, v, table, i32([0, new]), i32([400]), max_new=new)
+    cu, ln = i32([0, new]), i32([400])
+    torch.cuda.synchronize()
+    out2, lse2 = fa.fa_paged_fwd(q, k, v, table, cu, ln, max_new=new, stream=s)
+    s.synchronize()
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+# ------------------------------------------------------------------------------- together
+
+def test_serving_loop_matches_dense_attention():
+    """Prompts in chunks, decoding, finished requests, reused blocks: every step's attention against the
+    whole sequences, rotated and attended in 64 bits."""
+    torch.manual_seed(11)
+    Hq, Hkv, d, page, R = 8, 2, 64, 16, 5
+    inv, axis = spec(d, 1)
+    table = fa.RopeTable(inv, axis=axis)
+    kv = fa.PagedKV(R, 40, page, Hkv, d, max_blocks=20, layout="hnd")
+    hist = [[] for _ in range(R)]
+    steps = [[30, 0, 100, 7, 0], [1, 64, 50, 1, 0], [1, 1, 1, 1, 33], "2,3", [1, 1, 20, 0, 1], [1, 1, 1, 90, 1]]
+    for step in steps:
+        if step == "2,3":
+            kv.release(i32([0, 0, 1, 1, 0]))
+            hist[2], hist[3] = [], []
+            continue
+        T = sum(step) + 2
+        q, k, v = (torch.randn(T, h, d, device="cuda").to(torch.bfloat16) for h in (Hq, Hkv, Hkv))
+        kv.reserve(i32(step), T)
+        q_rot = torch.full((T, Hq, d), 0.0, device="cuda", dtype=torch.bfloat16)
+        kv.append(q, k, v, table, q_out=q_rot)
+        out, lse = kv.attend(q_rot, max_new=max(step))
+        at = 0
+        for r, n in enumerate(step):
+            if n:
+                hist[r].append((k[at:at + n], v[at:at + n]))
+                kk, vv = torch.cat([x[0] for x in hist[r]]), torch.cat([x[1] for x in hist[r]])
+                L = kk.shape[0]
+                kk = _paged.rope64(kk, torch.arange(L, device="cuda")[None], inv, axis, False).to(torch.bfloat16)
+                qq = _paged.rope64(q[at:at + n], torch.arange(L - n, L, device="cuda")[None], inv, axis, False)
+                # the kernel attends the rotated rows as rounded: the same rows here, but for ties
+                assert (q_rot[at:at + n].double() - qq).abs().max() <= 2.0 ** -7 * 8
+                one = torch.arange(blocks := -(-L // page), device="cuda", dtype=torch.int32)[None]
+                pad = blocks * page - L
+                kc = torch.cat([kk, kk.new_zeros(pad, Hkv, d)]).view(blocks, page, Hkv, d)
+                vc = torch.cat([vv, vv.new_zeros(pad, Hkv, d)]).view(blocks, page, Hkv, d)
+                got_k = kv.k_cache[kv.block_table[r, :blocks].long()].reshape(-1, Hkv, d)[:L]
+                assert (got_k.double() - kk.double()).abs().max() <= 2.0 ** -7 * 8   # a step of the largest value
+                want, z, t_out, t_lse = _paged.attend64(q_rot[at:at + n], kv.k_cache, kv.v_cache, kv.block_table[r:r + 1], [0, n], [L],
+                                                        causal=True, window=None, scale=d ** -0.5)
+                close(out[at:at + n], want, t_out)
+                close(lse[:, at:at + n], z, t_lse)
+                assert torch.equal(kv.v_cache[kv.block_table[r, :blocks].long()].reshape(-1, Hkv, d)[:L], vv)
+                del one, kc, vc
+            at += n
+        assert kv.seq_lens.tolist() == [sum(x[0].shape[0] for x in h) for h in hist]
+    held = sum(-(-n // page) for n in kv.seq_lens.tolist())
+    assert kv.free_count.item() == 40 - held
+    owned = [b for r in range(R) for b in kv.block_table[r, :-(-kv.seq_lens[r].item() // page)].tolist()]
+    assert sorted(owned + kv.free_blocks[:40 - held].tolist()) == list(range(40))
+
+
+def test_captured_decoding_steps():
+    """One decoding step captured into a graph and replayed: the same bits as the steps run eagerly."""
+    torch.manual_seed(12)
+    Hq, Hkv, d, page, R = 8, 2, 128, 16, 6
+    table = fa.RopeTable(spec(d, 1)[0])
+    prompt = [3, 70, 0, 16, 200, 1]
+    one = i32([1, 1, 0, 1, 1, 1])
+    T = 8
+
+    def start():
+        torch.manual_seed(13)
+        kv = fa.PagedKV(R, 64, page, Hkv, d, max_blocks=32)
+        n = sum(prompt)
+        k, v = (torch.randn(n, Hkv, d, device="cuda").to(torch.bfloat16) for _ in range(2))
+        kv.reserve(i32(prompt), n)
+        kv.append(None, k, v, table)
+        return kv
+
+    q, k, v = (torch.zeros(T, h, d, device="cuda", dtype=torch.bfloat16) for h in (Hq, Hkv, Hkv))
+    ws = torch.empty(fa.paged_workspace_bytes(Hq, Hkv, d), dtype=torch.uint8, device="cuda")
+
+    def step(kv, q_rot, out, lse):
+        kv.reserve(one, T)
+        kv.append(q, k, v, table, q_out=q_rot)
+        kv.attend(q_rot, max_new=1, out=out, lse=lse, workspace=ws)
+
+    def inputs(i):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(100 + i)
+        for x in (q, k, v):
+            x.copy_(torch.empty(x.shape, device="cuda").normal_(generator=g))
+
+    bufs = [(torch.zeros(T, Hq, d, device="cuda", dtype=torch.bfloat16), torch.zeros(T, Hq, d, device="cuda", dtype=torch.bfloat16),
+             torch.zeros(Hq, T, device="cuda")) for _ in range(2)]
+    eager, graphed = start(), start()
+    eager_out = []
+    for i in range(20):
+        inputs(i)
+        step(eager, *bufs[0])
+        eager_out.append((bufs[0][1].clone(), bufs[0][2].clone()))
+    side = torch.cuda.Stream()
+    graphed.reserve(i32([0] * R), T)   # makes the step's buffers; takes nothing
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        step(graphed, *bufs[1])
+    for i in range(20):
+        inputs(i)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(bufs[1][1], eager_out[i][0]) and torch.equal(bufs[1][2], eager_out[i][1])
+    assert graphed.seq_lens.tolist() == eager.seq_lens.tolist() == [p + 20 * o for p, o in zip(prompt, one.tolist())]
