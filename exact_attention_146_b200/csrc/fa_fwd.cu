@@ -121,26 +121,34 @@ bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
     return a0 < b0 + nb && b0 < a0 + na;
 }
 
-// 4-D view (d, H, N, B) of a [B, N, H, d] bf16 tensor, box (CW, heads, rows, 1): the box
-// lands in shared memory as heads*rows swizzled rows, row-major over (row, head).
-// elem: 0 bf16, 1 fp16, 2 E4M3 bytes.
-int encode_bnhd(CUtensorMap *m, const void *base, int d, int H, int N, int B, int cw, int rows, int heads,
-                int elem) {
+// 4-D view (d and the axes of `dims`, `strides` elements apart) of a 2-byte (elem 0: bf16, 1: fp16) or
+// E4M3 (2) tensor, box (cw, box[0 .. 2]), rows of cw elements swizzled over their own width.
+int encode_view(CUtensorMap *m, const void *base, int d, const long long (&dims)[3], const long long (&strides)[3],
+                int cw, const int (&box)[3], int elem) {
     EncodeTiledFn fn = encode_fn();
     if (fn == nullptr) return FA_ERR_CUDA;
-    const cuuint64_t dims[4] = {cuuint64_t(d), cuuint64_t(H), cuuint64_t(N), cuuint64_t(B)};
     const cuuint64_t es = elem == 2 ? 1 : 2;
-    const cuuint64_t strides[3] = {cuuint64_t(d) * es, cuuint64_t(H) * d * es, cuuint64_t(N) * H * d * es};
-    const cuuint32_t box[4] = {cuuint32_t(cw), cuuint32_t(heads), cuuint32_t(rows), 1};
+    const cuuint64_t gd[4] = {cuuint64_t(d), cuuint64_t(dims[0]), cuuint64_t(dims[1]), cuuint64_t(dims[2])};
+    const cuuint64_t gs[3] = {cuuint64_t(strides[0]) * es, cuuint64_t(strides[1]) * es, cuuint64_t(strides[2]) * es};
+    const cuuint32_t bx[4] = {cuuint32_t(cw), cuuint32_t(box[0]), cuuint32_t(box[1]), cuuint32_t(box[2])};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     const CUtensorMapSwizzle sw = (cw * es == 128) ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     const CUtensorMapDataType dt = elem == 2   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                    : elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    const CUresult r = fn(m, dt, 4, const_cast<void *>(base), dims, strides,
-                          box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = fn(m, dt, 4, const_cast<void *>(base), gd, gs, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
+// 4-D view (d, H, N, B) of a [B, N, H, d] bf16 tensor, box (CW, heads, rows, 1): the box
+// lands in shared memory as heads*rows swizzled rows, row-major over (row, head).
+// elem: 0 bf16, 1 fp16, 2 E4M3 bytes.
+int encode_bnhd(CUtensorMap *m, const void *base, int d, int H, int N, int B, int cw, int rows, int heads,
+                int elem) {
+    const long long dims[3] = {H, N, B}, strides[3] = {d, (long long)H * d, (long long)N * H * d};
+    const int box[3] = {heads, rows, 1};
+    return encode_view(m, base, d, dims, strides, cw, box, elem);
 }
 
 int zero_fill(void *dst, size_t bytes, float *lse, size_t n_lse, int num_sms, cudaStream_t st) {

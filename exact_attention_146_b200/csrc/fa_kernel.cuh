@@ -331,6 +331,25 @@ __device__ __forceinline__ bool warp_wait_bar(uint32_t bar, uint32_t parity, con
 // ------------------------------------------------------------------ TMA producer
 
 template <class C>
+__device__ __forceinline__ void producer_unwind(uint32_t sbase, uint32_t kv_cnt, const uint32_t (&qcnt)[2], const Ctl &ctl) {
+    auto bar = [&](int i) { return sbase + C::SMEM_BAR + 8u * uint32_t(i); };
+    // Unwinding after a timeout (here or in another role): let this thread's copies
+    // still in flight land before the CTA exits (the last load issued into each slot,
+    // and each Q tile).
+    const uint32_t first = kv_cnt > uint32_t(C::NS) ? kv_cnt - C::NS : 0u;
+    for (uint32_t n = first; n < kv_cnt; ++n)
+        wait_slow<kRoleControl>(bar(C::B_FULL + int(n % C::NS)), (n / C::NS) & 1u, ctl, kSiteProducerDrain,
+                  ctl.limit_ns / 10, true);
+#pragma unroll
+    for (int t = 0; t < C::NQT; ++t) {
+        const uint32_t first_q = qcnt[t] > uint32_t(C::NQB) ? qcnt[t] - C::NQB : 0u;
+        for (uint32_t n = first_q; n < qcnt[t]; ++n)
+            wait_slow<kRoleControl>(bar(C::B_QFULL + t * C::NQB + int(n % C::NQB)), (n / C::NQB) & 1u, ctl,
+                      kSiteProducerDrain, ctl.limit_ns / 10, true);
+    }
+}
+
+template <class C>
 __device__ void producer_role(const CUtensorMap *tm_q, const CUtensorMap *tm_k, const CUtensorMap *tm_v,
                               const FwdParams &p, uint32_t sbase, const Ctl &ctl) {
     auto bar = [&](int i) { return sbase + C::SMEM_BAR + 8u * uint32_t(i); };
@@ -384,22 +403,7 @@ __device__ void producer_role(const CUtensorMap *tm_q, const CUtensorMap *tm_k, 
             }
         }
     }
-    if (!ok || *ctl.abort_flag) {
-        // Unwinding after a timeout (here or in another role): let this thread's copies
-        // still in flight land before the CTA exits (the last load issued into each slot,
-        // and each Q tile).
-        const uint32_t first = kv_cnt > uint32_t(C::NS) ? kv_cnt - C::NS : 0u;
-        for (uint32_t n = first; n < kv_cnt; ++n)
-            wait_slow<kRoleControl>(bar(C::B_FULL + int(n % C::NS)), (n / C::NS) & 1u, ctl, kSiteProducerDrain,
-                      ctl.limit_ns / 10, true);
-#pragma unroll
-        for (int t = 0; t < C::NQT; ++t) {
-            const uint32_t first_q = qcnt[t] > uint32_t(C::NQB) ? qcnt[t] - C::NQB : 0u;
-            for (uint32_t n = first_q; n < qcnt[t]; ++n)
-                wait_slow<kRoleControl>(bar(C::B_QFULL + t * C::NQB + int(n % C::NQB)), (n / C::NQB) & 1u, ctl,
-                          kSiteProducerDrain, ctl.limit_ns / 10, true);
-        }
-    }
+    if (!ok || *ctl.abort_flag) producer_unwind<C>(sbase, kv_cnt, qcnt, ctl);
 }
 
 // ------------------------------------------------------------------ MMA issuer
@@ -444,8 +448,27 @@ __device__ __forceinline__ void issue_pv(uint32_t sbase, uint32_t tmem, int t, i
     }
 }
 
+// The units of a dense call, in the schedule's order.
 template <class C>
-__device__ void mma_role(const FwdParams &p, uint32_t sbase, uint32_t tmem, const Ctl &ctl) {
+struct DenseUnits {
+    using Unit = UnitInfo;
+    const FwdParams &p;
+    int r;
+    __device__ __forceinline__ bool next(UnitInfo &w) {
+        while (r * int(gridDim.x) < p.num_units) {
+            const int u = sched_unit(r++);
+            if (u >= p.num_units) continue;
+            w = decode_unit<C>(u, p);
+            return true;
+        }
+        return false;
+    }
+    // Called with the V tile j in shared memory at `tile`, before it is multiplied.
+    __device__ __forceinline__ void v_landed(const UnitInfo &, int, uint32_t) const {}
+};
+
+template <class C, class Units>
+__device__ void mma_role(Units units, uint32_t sbase, uint32_t tmem, const Ctl &ctl) {
     auto bar = [&](int i) { return sbase + C::SMEM_BAR + 8u * uint32_t(i); };
     // K/V loads arrive in the order K_0, V_0, K_1, V_1, ...: load n sits in slot n % NS
     // with phase (n / NS) & 1; kv_base is the first load index of the current unit.
@@ -475,11 +498,9 @@ __device__ void mma_role(const FwdParams &p, uint32_t sbase, uint32_t tmem, cons
         return warp_wait_bar<kRoleControl>(bar(C::B_PVDONE + t * C::SB + b), ((n / C::SB) - 1u) & 1u, ctl,
                                            kSitePvDone);
     };
-    for (int r = 0; ok && r * int(gridDim.x) < p.num_units; ++r) {
-        const int u = sched_unit(r);
-        if (u >= p.num_units) continue;
+    typename Units::Unit w;
+    while (ok && units.next(w)) {
         const uint32_t u_local = u_count++;
-        const UnitInfo w = decode_unit<C>(u, p);
         if (w.j_hi == w.j_lo) continue;
         int qbuf[2] = {0, 0};
         auto visits = [&](int t, int j) { return w.js[t] <= j && j < w.je[t]; };
@@ -556,6 +577,7 @@ __device__ void mma_role(const FwdParams &p, uint32_t sbase, uint32_t tmem, cons
         if (!ok) break;
         for (int j = w.j_lo; ok && j < w.j_hi; ++j) {
             if (!wait_load(kv_base + 2u * (j - w.j_lo) + 1u, slot_v)) { ok = false; break; }
+            units.v_landed(w, j, sbase + C::SMEM_KV + slot_v * C::KV_TILE);
             const int jn = j + C::SB;
             bool k_ready = false;
             if constexpr (C::SB == 2) {
@@ -716,20 +738,27 @@ __device__ __forceinline__ float exp_pack_store(const uint32_t (&s)[BC], float c
     return (a0 + a1) + (b0 + b1);
 }
 
+// The keys of a row tile: what this thread's row sees, and where the whole tile needs no mask.
+struct RowKeys {
+    int end;          // keys there are
+    int hi, lo;       // this row sees keys lo <= j <= hi (j < end)
+    int first_hi;     // the least hi of the tile's rows
+    int last_lo;      // the greatest lo of the tile's rows
+};
+
+// The online softmax of one query tile over its key tiles [js, je): S from TMEM, P back to it, O
+// rescaled there when the maximum has grown; m_ref and l are the row's.  scnt: S tiles consumed by this
+// role so far, ocnt: P V products of this tile before this unit.  False: a wait gave up.
 template <class C>
-__device__ void softmax_role(const FwdParams &p, const CUtensorMap *tm_o, uint32_t sbase, uint32_t tmem,
-                             const Ctl &ctl, int warp, int lane) {
+__device__ __forceinline__ bool softmax_tiles(uint32_t sbase, uint32_t tmem, const Ctl &ctl, int t, int quarter,
+                                              float c_log2, const RowKeys &keys, int js, int je, uint32_t &scnt,
+                                              uint32_t ocnt, float &m_ref, float &l) {
     constexpr int BC = C::BC;
     auto bar = [&](int i) { return sbase + C::SMEM_BAR + 8u * uint32_t(i); };
-    const int t = warp / 4;
-    const int quarter = warp % 4;                  // TMEM lanes 32*quarter .. +31
-    const int row_in_tile = quarter * 32 + lane;
     const uint32_t lane_off = uint32_t(quarter * 32) << 16;
     const uint32_t s_taddr0 = tmem + lane_off + uint32_t(C::SSHARE ? 0 : t * C::SB * BC);   // S buffer 0 of this tile
     const uint32_t p_taddr_sep = tmem + lane_off + uint32_t(C::P_COL0 + t * C::PCOLS);
     const uint32_t o_taddr = tmem + lane_off + uint32_t(C::O_COL0 + t * C::OST);
-    const float c_log2 = p.scale_log2;
-    uint32_t scnt = 0, ocnt = 0, ofin = 0;
     // Lazy rescale: O_t holds the sum up to block j-1 at the old reference max; wait for
     // that MMA (completion number `odone`), then scale this warp's rows by alpha (1 where
     // the max held).
@@ -748,6 +777,104 @@ __device__ void softmax_role(const FwdParams &p, const CUtensorMap *tm_o, uint32
         return true;
     };
 
+    for (int j = js; j < je; ++j) {
+        const int sb = int(scnt % C::SB);
+        const uint32_t s_taddr = s_taddr0 + uint32_t(sb * BC);
+        const uint32_t p_taddr = C::PSEP ? p_taddr_sep : s_taddr;
+        if (!warp_wait_bar(bar(C::B_SFULL + t * C::SB + sb), (scnt / C::SB) & 1u, ctl, kSiteSFull)) return false;
+        ++scnt;
+        sm100::tc_fence_after_sync();
+        uint32_t s[BC];
+        if constexpr (BC == 128) sm100::tmem_ld128_sync(s_taddr, s);
+        else sm100::tmem_ld64_sync(s_taddr, s);
+        if constexpr (C::SSHARE) {
+            // S is in registers: the shared buffer may take the next S (either tile's)
+            sm100::tc_fence_before_sync();
+            sm100::mbar_arrive(bar(C::B_SEMPTY));
+        }
+
+        const int k_lo = j * BC;
+        // boundary tiles: the key tail, the causal diagonal, the window's lower edge
+        const bool need_mask = (k_lo + BC > keys.end) || (k_lo + BC - 1 > keys.first_hi) || (k_lo < keys.last_lo);
+        float alpha = 1.f;
+        bool need_rescale = false;
+        float row_sum;
+        {
+            if (need_mask) {
+#pragma unroll
+                for (int i = 0; i < BC; ++i) {
+                    const int key = k_lo + i;
+                    if (key > keys.hi || key >= keys.end || key < keys.lo) s[i] = __float_as_uint(-INFINITY);
+                }
+            }
+            // Row max: eight independent 3-input-max chains, then a short tree, so
+            // the dependency depth stays small.
+            float mx[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) mx[c] = fmaxf(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
+#pragma unroll
+            for (int i = 16; i < BC; i += 16)
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    mx[c] = sm100::max3(mx[c], __uint_as_float(s[i + 2 * c]), __uint_as_float(s[i + 2 * c + 1]));
+            const float mx_s = fmaxf(sm100::max3(mx[0], mx[1], mx[2]), sm100::max3(mx[3], mx[4], sm100::max3(mx[5], mx[6], mx[7]))) * c_log2;
+            if (j == js) {
+                m_ref = mx_s;
+            } else if (mx_s > m_ref + kRescaleLog2) {
+                alpha = sm100::ex2_approx(m_ref - mx_s);
+                m_ref = mx_s;
+                need_rescale = true;
+            }
+            // with a split hand-off, O is rescaled before any of P is handed over (the
+            // first P V MMAs accumulate into O while the rest of P is computed)
+            if constexpr (C::PSPLIT)
+                if (!rescale_o(need_rescale, alpha, ocnt + uint32_t(j - js) - 1u)) return false;
+            const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
+            const uint32_t half_bar = bar(C::B_PHALF + t * C::SB + sb);
+            if constexpr (C::SSHARE) {
+                // P_t's columns are free once the previous P_t V has completed (the
+                // first P of a unit: the epilogue's wait for the unit's last P V)
+                constexpr int kChunks = C::PCOLS / 32;
+                uint32_t pk_all[kChunks][32];
+                if constexpr (C::FP8)
+                    row_sum = exp_pack_store_e4m3<BC, true>(s, c_log2, neg_m, p_taddr, pk_all);
+                else
+                    row_sum = need_mask
+                                  ? exp_pack_store<BC, C::SOFT_EXP, false, C::F16, false, true>(s, c_log2, neg_m, p_taddr, 0, pk_all)
+                                  : exp_pack_store<BC, C::SOFT_EXP, true, C::F16, false, true>(s, c_log2, neg_m, p_taddr, 0, pk_all);
+                if (j > js && !warp_wait_bar(bar(C::B_ODONE + t), (ocnt + uint32_t(j - js) - 1u) & 1u, ctl, kSiteODone))
+                    return false;
+                sm100::tc_fence_after_sync();
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) sm100::tmem_st32(p_taddr + uint32_t(32 * c), pk_all[c]);
+            } else if constexpr (C::FP8)
+                row_sum = exp_pack_store_e4m3<BC>(s, c_log2, neg_m, p_taddr);
+            else
+                row_sum = need_mask
+                              ? exp_pack_store<BC, C::SOFT_EXP, false, C::F16, C::PSPLIT>(s, c_log2, neg_m, p_taddr, half_bar)
+                              : exp_pack_store<BC, C::SOFT_EXP, true, C::F16, C::PSPLIT>(s, c_log2, neg_m, p_taddr, half_bar);
+        }
+        l = l * alpha + row_sum;
+        if constexpr (!C::PSPLIT)
+            if (!rescale_o(need_rescale, alpha, ocnt + uint32_t(j - js) - 1u)) return false;
+        sm100::tmem_st_wait();
+        sm100::tc_fence_before_sync();
+        sm100::mbar_arrive(bar(C::B_PFULL + t * C::SB + sb));
+    }
+    return true;
+}
+
+template <class C>
+__device__ void softmax_role(const FwdParams &p, const CUtensorMap *tm_o, uint32_t sbase, uint32_t tmem,
+                             const Ctl &ctl, int warp, int lane) {
+    auto bar = [&](int i) { return sbase + C::SMEM_BAR + 8u * uint32_t(i); };
+    const int t = warp / 4;
+    const int quarter = warp % 4;                  // TMEM lanes 32*quarter .. +31
+    const int row_in_tile = quarter * 32 + lane;
+    const uint32_t lane_off = uint32_t(quarter * 32) << 16;
+    const uint32_t o_taddr = tmem + lane_off + uint32_t(C::O_COL0 + t * C::OST);
+    const float c_log2 = p.scale_log2;
+    uint32_t scnt = 0, ocnt = 0, ofin = 0;
     for (int r = 0; r * int(gridDim.x) < p.num_units; ++r) {
         const int u = sched_unit(r);
         if (u >= p.num_units) continue;
@@ -767,91 +894,8 @@ __device__ void softmax_role(const FwdParams &p, const CUtensorMap *tm_o, uint32
         float m_ref = -INFINITY;                   // reference max, log2 units (scaled)
         float l = 0.f;                             // running sum of 2^(s*c - m_ref)
 
-        for (int j = js; j < je; ++j) {
-            const int sb = int(scnt % C::SB);
-            const uint32_t s_taddr = s_taddr0 + uint32_t(sb * BC);
-            const uint32_t p_taddr = C::PSEP ? p_taddr_sep : s_taddr;
-            if (!warp_wait_bar(bar(C::B_SFULL + t * C::SB + sb), (scnt / C::SB) & 1u, ctl, kSiteSFull)) goto unwind;
-            ++scnt;
-            sm100::tc_fence_after_sync();
-            uint32_t s[BC];
-            if constexpr (BC == 128) sm100::tmem_ld128_sync(s_taddr, s);
-            else sm100::tmem_ld64_sync(s_taddr, s);
-            if constexpr (C::SSHARE) {
-                // S is in registers: the shared buffer may take the next S (either tile's)
-                sm100::tc_fence_before_sync();
-                sm100::mbar_arrive(bar(C::B_SEMPTY));
-            }
-
-            const int k_lo = j * BC;
-            // boundary tiles: the key tail, the causal diagonal, the window's lower edge
-            const bool need_mask = (k_lo + BC > p.Nk) || (p.causal && k_lo + BC - 1 > q_lo + diag) ||
-                                   (k_lo < tile_lo_hi);
-            float alpha = 1.f;
-            bool need_rescale = false;
-            float row_sum;
-            {
-                if (need_mask) {
-#pragma unroll
-                    for (int i = 0; i < BC; ++i) {
-                        const int key = k_lo + i;
-                        if (key > row_lim || key >= p.Nk || key < row_lo) s[i] = __float_as_uint(-INFINITY);
-                    }
-                }
-                // Row max: eight independent 3-input-max chains, then a short tree, so
-                // the dependency depth stays small.
-                float mx[8];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) mx[c] = fmaxf(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
-#pragma unroll
-                for (int i = 16; i < BC; i += 16)
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        mx[c] = sm100::max3(mx[c], __uint_as_float(s[i + 2 * c]), __uint_as_float(s[i + 2 * c + 1]));
-                const float mx_s = fmaxf(sm100::max3(mx[0], mx[1], mx[2]), sm100::max3(mx[3], mx[4], sm100::max3(mx[5], mx[6], mx[7]))) * c_log2;
-                if (j == js) {
-                    m_ref = mx_s;
-                } else if (mx_s > m_ref + kRescaleLog2) {
-                    alpha = sm100::ex2_approx(m_ref - mx_s);
-                    m_ref = mx_s;
-                    need_rescale = true;
-                }
-                // with a split hand-off, O is rescaled before any of P is handed over (the
-                // first P V MMAs accumulate into O while the rest of P is computed)
-                if constexpr (C::PSPLIT)
-                    if (!rescale_o(need_rescale, alpha, ocnt + uint32_t(j - js) - 1u)) goto unwind;
-                const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
-                const uint32_t half_bar = bar(C::B_PHALF + t * C::SB + sb);
-                if constexpr (C::SSHARE) {
-                    // P_t's columns are free once the previous P_t V has completed (the
-                    // first P of a unit: the epilogue's wait for the unit's last P V)
-                    constexpr int kChunks = C::PCOLS / 32;
-                    uint32_t pk_all[kChunks][32];
-                    if constexpr (C::FP8)
-                        row_sum = exp_pack_store_e4m3<BC, true>(s, c_log2, neg_m, p_taddr, pk_all);
-                    else
-                        row_sum = need_mask
-                                      ? exp_pack_store<BC, C::SOFT_EXP, false, C::F16, false, true>(s, c_log2, neg_m, p_taddr, 0, pk_all)
-                                      : exp_pack_store<BC, C::SOFT_EXP, true, C::F16, false, true>(s, c_log2, neg_m, p_taddr, 0, pk_all);
-                    if (j > js && !warp_wait_bar(bar(C::B_ODONE + t), (ocnt + uint32_t(j - js) - 1u) & 1u, ctl, kSiteODone))
-                        goto unwind;
-                    sm100::tc_fence_after_sync();
-#pragma unroll
-                    for (int c = 0; c < kChunks; ++c) sm100::tmem_st32(p_taddr + uint32_t(32 * c), pk_all[c]);
-                } else if constexpr (C::FP8)
-                    row_sum = exp_pack_store_e4m3<BC>(s, c_log2, neg_m, p_taddr);
-                else
-                    row_sum = need_mask
-                                  ? exp_pack_store<BC, C::SOFT_EXP, false, C::F16, C::PSPLIT>(s, c_log2, neg_m, p_taddr, half_bar)
-                                  : exp_pack_store<BC, C::SOFT_EXP, true, C::F16, C::PSPLIT>(s, c_log2, neg_m, p_taddr, half_bar);
-            }
-            l = l * alpha + row_sum;
-            if constexpr (!C::PSPLIT)
-                if (!rescale_o(need_rescale, alpha, ocnt + uint32_t(j - js) - 1u)) goto unwind;
-            sm100::tmem_st_wait();
-            sm100::tc_fence_before_sync();
-            sm100::mbar_arrive(bar(C::B_PFULL + t * C::SB + sb));
-        }
+        const RowKeys keys{p.Nk, row_lim, row_lo, p.causal ? q_lo + diag : 0x7fffffff, tile_lo_hi};
+        if (!softmax_tiles<C>(sbase, tmem, ctl, t, quarter, c_log2, keys, js, je, scnt, ocnt, m_ref, l)) goto unwind;
 
         // epilogue: O / l -> bf16 -> out, LSE -> lse
         if (nk > 0) {
@@ -962,6 +1006,33 @@ unwind:
 
 // ------------------------------------------------------------------ kernel
 
+// By one thread, before the roles start.
+template <class C>
+__device__ __forceinline__ void init_barriers(uint32_t sbase) {
+    auto bar = [&](int i) { return sbase + C::SMEM_BAR + 8u * uint32_t(i); };
+    for (int s = 0; s < C::NS; ++s) {
+        sm100::mbar_init(bar(C::B_FULL + s), 1);
+        sm100::mbar_init(bar(C::B_EMPTY + s), 1);
+    }
+    for (int i = 0; i < C::NQT * C::NQB; ++i) {
+        sm100::mbar_init(bar(C::B_QFULL + i), 1);
+        sm100::mbar_init(bar(C::B_QEMPTY + i), 1);
+    }
+    for (int i = 0; i < C::NQT * C::SB; ++i) {
+        sm100::mbar_init(bar(C::B_SFULL + i), 1);
+        sm100::mbar_init(bar(C::B_PFULL + i), 128);
+        sm100::mbar_init(bar(C::B_PHALF + i), 128);
+        sm100::mbar_init(bar(C::B_PVDONE + i), 1);
+    }
+    for (int t = 0; t < C::NQT; ++t) {
+        sm100::mbar_init(bar(C::B_ODONE + t), 1);
+        sm100::mbar_init(bar(C::B_OFINAL + t), 1);
+        sm100::mbar_init(bar(C::B_OEMPTY + t), 128);
+    }
+    sm100::mbar_init(bar(C::B_DRAIN), 1);
+    sm100::mbar_init(bar(C::B_SEMPTY), 128);
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
 fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -977,28 +1048,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     const Ctl ctl{abort_flag, p.status, C::FAULT ? uint64_t(p.wait_limit_ns) : kWaitLimitNs};
 
     if (threadIdx.x == 0) {
-        auto bar = [&](int i) { return sbase + C::SMEM_BAR + 8u * uint32_t(i); };
-        for (int s = 0; s < C::NS; ++s) {
-            sm100::mbar_init(bar(C::B_FULL + s), 1);
-            sm100::mbar_init(bar(C::B_EMPTY + s), 1);
-        }
-        for (int i = 0; i < C::NQT * C::NQB; ++i) {
-            sm100::mbar_init(bar(C::B_QFULL + i), 1);
-            sm100::mbar_init(bar(C::B_QEMPTY + i), 1);
-        }
-        for (int i = 0; i < C::NQT * C::SB; ++i) {
-            sm100::mbar_init(bar(C::B_SFULL + i), 1);
-            sm100::mbar_init(bar(C::B_PFULL + i), 128);
-            sm100::mbar_init(bar(C::B_PHALF + i), 128);
-            sm100::mbar_init(bar(C::B_PVDONE + i), 1);
-        }
-        for (int t = 0; t < C::NQT; ++t) {
-            sm100::mbar_init(bar(C::B_ODONE + t), 1);
-            sm100::mbar_init(bar(C::B_OFINAL + t), 1);
-            sm100::mbar_init(bar(C::B_OEMPTY + t), 128);
-        }
-        sm100::mbar_init(bar(C::B_DRAIN), 1);
-        sm100::mbar_init(bar(C::B_SEMPTY), 128);
+        init_barriers<C>(sbase);
         *abort_flag = 0;
         sm100::fence_mbar_init();
     }
@@ -1019,7 +1069,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         if (warp == C::TMA_WARP) {
             producer_role<C>(&tm_q, &tm_k, &tm_v, p, sbase, ctl);
         } else if (warp == C::MMA_WARP) {
-            mma_role<C>(p, sbase, tmem, ctl);
+            mma_role<C>(DenseUnits<C>{p, 0}, sbase, tmem, ctl);
         }
     }
     __syncwarp();
@@ -1096,7 +1146,7 @@ __global__ void __launch_bounds__(256) fa_splitkv_merge_kernel(const float *o_pa
 }
 
 // Nk == 0: no key at all, so every output row is 0 and every LSE is -inf.
-__global__ void fa_no_keys_kernel(uint4 *out, size_t n_vec16, float *lse, size_t n_lse) {
+static __global__ void fa_no_keys_kernel(uint4 *out, size_t n_vec16, float *lse, size_t n_lse) {
     const size_t stride = size_t(gridDim.x) * blockDim.x;
     for (size_t i = size_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n_vec16; i += stride)
         out[i] = make_uint4(0u, 0u, 0u, 0u);

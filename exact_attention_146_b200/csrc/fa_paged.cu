@@ -1,5 +1,6 @@
 // fa_paged.cu -- attention of new tokens over a paged cache (fa_paged_fwd, declared in include/fa.h):
-// argument checks, workspace layout and launches of the kernels in fa_paged_rows.cuh.
+// argument checks, workspace layout, choice and launches of the kernels in fa_paged_rows.cuh (few rows)
+// and fa_paged_tiles.cuh (many).
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -11,6 +12,7 @@
 #include "fa_cache.h"
 #include "fa_host.h"
 #include "fa_paged_rows.cuh"
+#include "fa_paged_tiles.cuh"
 
 namespace {
 
@@ -74,11 +76,96 @@ int launch_rows(PagedParams p, void *workspace, int ctas, int dev, cudaStream_t 
     p.lse_part = reinterpret_cast<float *>(static_cast<char *>(workspace) + part_o_bytes(workers, kRowRows, C::D));
     fa_paged_rows_kernel<C><<<unsigned(ctas), C::THREADS, C::SMEM, st>>>(p);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-    return launch_after(fa_paged_merge_kernel<C::D, C::F16, kRowRows, kRowKeys>, dim3(unsigned(workers - 1)), 128, p, st);
+    return launch_after(fa_paged_merge_kernel<C::D, C::F16, kRowRows, kRowRows, kRowKeys>, dim3(unsigned(workers - 1)), 128, p, st);
+}
+
+// The dense forward's tilings (fa_fwd.cu says why each).
+template <bool H> using Tile32 = TileCfg<32, 128, 2, 8, 2, 1, true, 2, H>;
+template <bool H> using Tile64 = TileCfg<64, 128, 2, 8, 2, 1, true, 2, H>;
+template <bool H> using Tile80 = TileCfg<80, 128, 2, 4, 1, 1, true, 0, H, false, false, true>;
+template <bool H> using Tile96 = TileCfg<96, 128, 2, 4, 1, 1, true, 0, H, false, false, true>;
+template <bool H> using Tile128 = TileCfg<128, 128, 2, 4, 1, 1, true, 0, H, false, false, true>;
+template <bool H> using Tile192 = TileCfg<192, 64, 2, 4, 1, 1, true, 0, H, false, false, true>;
+template <bool H> using Tile256 = TileCfg<256, 64, 1, 4, 1, 2, false, 0, H>;
+
+// The largest power of two, up to a key tile, that divides a page.
+int box_rows(int page, int most) {
+    int g = 1;
+    while (g < most && page % (2 * g) == 0) g *= 2;
+    return g;
+}
+
+// A [T, H, d] array of rows `stride` apart: box (cw columns, heads, rows).
+struct View {
+    const void *base;
+    long long dims[3], strides[3];   // elements; the axes after d
+    int box[3];
+};
+
+template <class C>
+int launch_tiles(const PagedParams &base, const View &q, View kv, const void *v, void *workspace, int ctas, int dev, cudaStream_t st) {
+    static int ready[kMaxDevices] = {};   // 0 unknown, 1 usable, -1 not
+    {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        if (ready[dev] == 0) {
+            cudaFuncAttributes a{};
+            if (cudaFuncSetAttribute(fa_paged_tiles_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess ||
+                cudaFuncGetAttributes(&a, fa_paged_tiles_kernel<C>) != cudaSuccess) {
+                cudaGetLastError();
+                return FA_ERR_CUDA;
+            }
+            // the register split inside the kernel counts on exactly this launch budget
+            ready[dev] = (!C::REALLOC_REGS || a.numRegs == C::LAUNCH_REGS) ? 1 : -1;
+        }
+        if (ready[dev] != 1) return FA_ERR_CUDA;
+    }
+    PagedTileParams p{};
+    static_cast<PagedParams &>(p) = base;
+    p.tq = kBlockQ / p.pack;
+    p.plan.groups = p.Hq / p.pack;
+    p.plan.tpb = C::NQT * p.tq;
+    p.plan.workers = ctas;
+    p.box_rows = box_rows(p.page, C::BC);
+    p.slot_first = p.slot_stride < p.head_stride ? 1 : 0;
+    kv.box[p.slot_first ? 0 : 1] = p.box_rows;
+    constexpr int rows = C::NQT * kBlockQ;
+    p.o_part = static_cast<float *>(workspace);
+    p.lse_part = reinterpret_cast<float *>(static_cast<char *>(workspace) + part_o_bytes(ctas, rows, C::D));
+    CUtensorMap mq, mk, mv;
+    int rc;
+    const int elem = C::F16 ? 1 : 0;
+    if ((rc = encode_view(&mq, q.base, C::D, q.dims, q.strides, C::CW, q.box, elem)) != FA_OK) return rc;
+    if ((rc = encode_view(&mk, kv.base, C::D, kv.dims, kv.strides, C::CW, kv.box, elem)) != FA_OK) return rc;
+    if ((rc = encode_view(&mv, v, C::D, kv.dims, kv.strides, C::CW, kv.box, elem)) != FA_OK) return rc;
+    fa_paged_tiles_kernel<C><<<unsigned(ctas), C::THREADS, C::SMEM_BYTES, st>>>(mq, mk, mv, p);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    if (ctas < 2) return FA_OK;
+    return launch_after(fa_paged_merge_kernel<C::D, C::F16, rows, kBlockQ, C::BC>, dim3(unsigned(ctas - 1), rows / 16), 128,
+                        static_cast<const PagedParams &>(p), st);
 }
 
 template <bool F16>
-int dispatch(const PagedParams &p, int d, void *workspace, int ctas, int dev, cudaStream_t st) {
+int dispatch_tiles(PagedParams p, int d, int num_blocks, int Hkv, void *workspace, int ctas, int dev, cudaStream_t st) {
+    p.pack = largest_divisor(p.n_rep, kBlockQ);
+    const View q{p.q, {p.Hq, p.plan.T, 1}, {d, p.q_stride, p.q_stride * p.plan.T}, {p.pack, kBlockQ / p.pack, 1}};
+    View kv{p.k, {Hkv, p.page, num_blocks}, {p.head_stride, p.slot_stride, p.block_stride}, {1, 1, 1}};
+    if (p.slot_stride < p.head_stride) {
+        std::swap(kv.dims[0], kv.dims[1]);
+        std::swap(kv.strides[0], kv.strides[1]);
+    }
+    switch (d) {
+        case 32: return launch_tiles<Tile32<F16>>(p, q, kv, p.v, workspace, ctas, dev, st);
+        case 64: return launch_tiles<Tile64<F16>>(p, q, kv, p.v, workspace, ctas, dev, st);
+        case 80: return launch_tiles<Tile80<F16>>(p, q, kv, p.v, workspace, ctas, dev, st);
+        case 96: return launch_tiles<Tile96<F16>>(p, q, kv, p.v, workspace, ctas, dev, st);
+        case 128: return launch_tiles<Tile128<F16>>(p, q, kv, p.v, workspace, ctas, dev, st);
+        case 192: return launch_tiles<Tile192<F16>>(p, q, kv, p.v, workspace, ctas, dev, st);
+        default: return launch_tiles<Tile256<F16>>(p, q, kv, p.v, workspace, ctas, dev, st);
+    }
+}
+
+template <bool F16>
+int dispatch_rows(const PagedParams &p, int d, void *workspace, int ctas, int dev, cudaStream_t st) {
     switch (d) {
         case 32: return launch_rows<RowCfg<32, F16>>(p, workspace, ctas, dev, st);
         case 64: return launch_rows<RowCfg<64, F16>>(p, workspace, ctas, dev, st);
@@ -150,7 +237,13 @@ int paged_fwd(const void *q, long long q_stride, const fa_paged_cache *cache, co
     p.scale_log2 = scale * 1.4426950408889634f;
     const int ctas = std::min(dev->num_sms, kMaxPagedCtas);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return f16 ? dispatch<true>(p, d, workspace, ctas, dev_id, st) : dispatch<false>(p, d, workspace, ctas, dev_id, st);
+    // Row tiles of 128 need pages of whole swizzle atoms (8 slots); any other page, and calls of few rows,
+    // take the kernel that gathers key by key.
+    const bool tiles = (long long)max_new * p.n_rep > kRowRows && p.page % 8 == 0 && p.num_blocks > 0;
+    if (tiles)
+        return f16 ? dispatch_tiles<true>(p, d, p.num_blocks, Hkv, workspace, ctas, dev_id, st)
+                   : dispatch_tiles<false>(p, d, p.num_blocks, Hkv, workspace, ctas, dev_id, st);
+    return f16 ? dispatch_rows<true>(p, d, workspace, ctas, dev_id, st) : dispatch_rows<false>(p, d, workspace, ctas, dev_id, st);
 }
 
 }  // namespace
@@ -159,7 +252,7 @@ extern "C" {
 
 size_t fa_paged_workspace_bytes(int Hq, int Hkv, int d) {
     if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || fa_tile_config(d, nullptr, nullptr, nullptr, nullptr) != FA_OK) return 0;
-    return part_bytes(kMaxRowWorkers, kRowRows, d);
+    return std::max(part_bytes(kMaxRowWorkers, kRowRows, d), part_bytes(kMaxPagedCtas, d == 256 ? kBlockQ : 2 * kBlockQ, d));
 }
 
 int fa_paged_fwd(const void *q, long long q_stride, const fa_paged_cache *cache, const int *block_table,

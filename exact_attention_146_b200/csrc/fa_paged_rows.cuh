@@ -338,9 +338,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) fa_paged_rows_kernel(const __gr
 }
 
 // Merges the pieces of every unit that a cut crosses: one block a cut, the first cut in a unit
-// does it.  ROWS: rows a unit has in the workspace; KS: keys a step; the block's warps take rows
-// blockIdx.y * ROWS / gridDim.y ....
-template <int D, bool F16, int ROWS, int KS>
+// does it.  ROWS: rows a unit has in the workspace, in tiles of TILE (each TILE / pack tokens of
+// `pack` heads); KS: keys a step; the block's warps take rows blockIdx.y * ROWS / gridDim.y ....
+template <int D, bool F16, int ROWS, int TILE, int KS>
 __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const __grid_constant__ PagedParams p) {
     __shared__ PlanScan<128> scan;
     const long long total = plan_scan<KS>(p.plan, scan, int(threadIdx.x), false);
@@ -359,8 +359,9 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const __grid_consta
     const int lane = int(threadIdx.x) % 32;
     const int per_y = ROWS / int(gridDim.y);
     for (int row = int(blockIdx.y) * per_y + int(threadIdx.x) / 32; row < (int(blockIdx.y) + 1) * per_y; row += 4) {
-        const int i = row / p.pack, token = u.b * p.plan.tpb + i, head = u.g * p.pack + row - i * p.pack;
-        if (i >= p.plan.tpb || token >= u.q.n) break;
+        const int tile = row / TILE, in_tile = row - tile * TILE, i = in_tile / p.pack, tq = TILE / p.pack;
+        const int token = u.b * p.plan.tpb + tile * tq + i, head = u.g * p.pack + in_tile - i * p.pack;
+        if (i >= tq || token >= u.q.n) continue;
         auto slot_of = [&](int part) { return part == 0 ? first_slot : 2 * (w - 1 + part); };
         float m = -INFINITY;
         for (int s = lane; s < parts; s += 32) m = fmaxf(m, p.lse_part[(long long)slot_of(s) * ROWS + row]);
