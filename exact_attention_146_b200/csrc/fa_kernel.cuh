@@ -801,10 +801,15 @@ __device__ __forceinline__ bool softmax_tiles(uint32_t sbase, uint32_t tmem, con
         float row_sum;
         {
             if (need_mask) {
+                const int top = min(keys.hi, keys.end - 1) - k_lo;   // the row's last key in this tile
 #pragma unroll
-                for (int i = 0; i < BC; ++i) {
-                    const int key = k_lo + i;
-                    if (key > keys.hi || key >= keys.end || key < keys.lo) s[i] = __float_as_uint(-INFINITY);
+                for (int i = 0; i < BC; ++i)
+                    if (i > top) s[i] = __float_as_uint(-INFINITY);
+                if (k_lo < keys.last_lo) {
+                    const int bottom = keys.lo - k_lo;
+#pragma unroll
+                    for (int i = 0; i < BC; ++i)
+                        if (i < bottom) s[i] = __float_as_uint(-INFINITY);
                 }
             }
             // Row max: eight independent 3-input-max chains, then a short tree, so
@@ -838,6 +843,8 @@ __device__ __forceinline__ bool softmax_tiles(uint32_t sbase, uint32_t tmem, con
                 uint32_t pk_all[kChunks][32];
                 if constexpr (C::FP8)
                     row_sum = exp_pack_store_e4m3<BC, true>(s, c_log2, neg_m, p_taddr, pk_all);
+                else if constexpr (C::SOFT_EXP == 0)   // masked tiles take the same instructions: one copy of them
+                    row_sum = exp_pack_store<BC, 0, false, C::F16, false, true>(s, c_log2, neg_m, p_taddr, 0, pk_all);
                 else
                     row_sum = need_mask
                                   ? exp_pack_store<BC, C::SOFT_EXP, false, C::F16, false, true>(s, c_log2, neg_m, p_taddr, 0, pk_all)
@@ -849,6 +856,8 @@ __device__ __forceinline__ bool softmax_tiles(uint32_t sbase, uint32_t tmem, con
                 for (int c = 0; c < kChunks; ++c) sm100::tmem_st32(p_taddr + uint32_t(32 * c), pk_all[c]);
             } else if constexpr (C::FP8)
                 row_sum = exp_pack_store_e4m3<BC>(s, c_log2, neg_m, p_taddr);
+            else if constexpr (C::SOFT_EXP == 0)
+                row_sum = exp_pack_store<BC, 0, false, C::F16, C::PSPLIT>(s, c_log2, neg_m, p_taddr, half_bar);
             else
                 row_sum = need_mask
                               ? exp_pack_store<BC, C::SOFT_EXP, false, C::F16, C::PSPLIT>(s, c_log2, neg_m, p_taddr, half_bar)

@@ -27,6 +27,7 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 // and last unit).
 size_t part_o_bytes(int workers, int rows, int d) { return align256(size_t(workers) * 2 * rows * d * 4); }
 size_t part_bytes(int workers, int rows, int d) { return part_o_bytes(workers, rows, d) + align256(size_t(workers) * 2 * rows * 4); }
+size_t job_bytes(int workers) { return align256(size_t(workers) * sizeof(MergeJob)); }
 
 int largest_divisor(int n, int most) {
     for (int x = std::min(n, most); x > 1; --x)
@@ -36,47 +37,64 @@ int largest_divisor(int n, int most) {
 
 // Launches `kern` so that its blocks may be set up while the kernel before it in the stream still
 // runs (it waits for that kernel's end itself, by griddepcontrol.wait).
-template <class P>
-int launch_after(void (*kern)(P), dim3 grid, int threads, const P &p, cudaStream_t st) {
+template <class... P, class... A>
+int launch_after(void (*kern)(P...), unsigned grid, int threads, size_t smem, cudaStream_t st, A... args) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
+    cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kern, args...) != cudaSuccess) {
         cudaGetLastError();
         return FA_ERR_CUDA;
     }
     return FA_OK;
 }
 
-template <class C>
-int launch_rows(PagedParams p, void *workspace, int ctas, int dev, cudaStream_t st) {
-    static bool smem_set[kMaxDevices] = {};
-    {
-        std::lock_guard<std::mutex> lock(g_mutex);
-        if (!smem_set[dev]) {
-            if (cudaFuncSetAttribute(fa_paged_rows_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) {
-                cudaGetLastError();
-                return FA_ERR_CUDA;
-            }
-            smem_set[dev] = true;
+// What is kept per kernel and device: its shared-memory limit has been raised, and its registers are
+// those that it was written for (0 not looked at, 1 usable, -1 not).
+template <class Kernel>
+int make_ready(Kernel kern, int smem, int regs, int &state) {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (state == 0) {
+        cudaFuncAttributes a{};
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+            cudaFuncGetAttributes(&a, kern) != cudaSuccess) {
+            cudaGetLastError();
+            return FA_ERR_CUDA;
         }
+        state = (regs == 0 || a.numRegs == regs) ? 1 : -1;
     }
-    const int workers = ctas * C::WARPS;
+    return state == 1 ? FA_OK : FA_ERR_CUDA;
+}
+
+// The kernel of few rows; fills what it adds to `p`.
+template <class C>
+int launch_rows(PagedParams &p, char *workspace, int ctas, int dev, cudaStream_t st) {
+    static int state[kMaxDevices] = {};
+    const int rc = make_ready(fa_paged_rows_kernel<C>, C::SMEM, 0, state[dev]);
+    if (rc != FA_OK) return rc;
     p.pack = largest_divisor(p.n_rep, kRowRows);
     p.plan.groups = p.Hq / p.pack;
     p.plan.tpb = kRowRows / p.pack;
-    p.plan.workers = workers;
-    p.o_part = static_cast<float *>(workspace);
-    p.lse_part = reinterpret_cast<float *>(static_cast<char *>(workspace) + part_o_bytes(workers, kRowRows, C::D));
+    p.plan.workers = ctas * C::WARPS;
+    p.o_part = reinterpret_cast<float *>(workspace);
+    p.lse_part = reinterpret_cast<float *>(workspace + part_o_bytes(p.plan.workers, kRowRows, C::D));
+    p.jobs = reinterpret_cast<MergeJob *>(workspace + part_bytes(p.plan.workers, kRowRows, C::D));
     fa_paged_rows_kernel<C><<<unsigned(ctas), C::THREADS, C::SMEM, st>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-    return launch_after(fa_paged_merge_kernel<C::D, C::F16, kRowRows, kRowRows, kRowKeys>, dim3(unsigned(workers - 1)), 128, p, st);
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+template <int D, bool F16>
+int launch_rows_only(PagedParams p, char *workspace, int ctas, int dev, cudaStream_t st) {
+    const int rc = launch_rows<RowCfg<D, F16>>(p, workspace, ctas, dev, st);
+    if (rc != FA_OK) return rc;
+    return launch_after(fa_paged_merge_rows_kernel<D, F16>, unsigned(p.plan.workers - 1), 256, 0, st, p);
 }
 
 // The dense forward's tilings (fa_fwd.cu says why each).
@@ -102,50 +120,54 @@ struct View {
     int box[3];
 };
 
+// Chunks on the tensor cores; requests of at most `few` new tokens (few > 0) by the kernel of few rows
+// before it, in the same stream but not in its way: the tile kernel's CTAs start as the other's end.
 template <class C>
-int launch_tiles(const PagedParams &base, const View &q, View kv, const void *v, void *workspace, int ctas, int dev, cudaStream_t st) {
-    static int ready[kMaxDevices] = {};   // 0 unknown, 1 usable, -1 not
-    {
-        std::lock_guard<std::mutex> lock(g_mutex);
-        if (ready[dev] == 0) {
-            cudaFuncAttributes a{};
-            if (cudaFuncSetAttribute(fa_paged_tiles_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) != cudaSuccess ||
-                cudaFuncGetAttributes(&a, fa_paged_tiles_kernel<C>) != cudaSuccess) {
-                cudaGetLastError();
-                return FA_ERR_CUDA;
-            }
-            // the register split inside the kernel counts on exactly this launch budget
-            ready[dev] = (!C::REALLOC_REGS || a.numRegs == C::LAUNCH_REGS) ? 1 : -1;
-        }
-        if (ready[dev] != 1) return FA_ERR_CUDA;
-    }
+int launch_tiles(const PagedParams &base, const View &q, View kv, const void *v, int few, char *workspace, int ctas, int dev,
+                 cudaStream_t st) {
+    static int state[kMaxDevices] = {};
+    // the register split inside the kernel counts on exactly this launch budget
+    int rc = make_ready(fa_paged_tiles_kernel<C>, C::SMEM_BYTES, C::REALLOC_REGS ? C::LAUNCH_REGS : 0, state[dev]);
+    if (rc != FA_OK) return rc;
     PagedTileParams p{};
     static_cast<PagedParams &>(p) = base;
     p.tq = kBlockQ / p.pack;
     p.plan.groups = p.Hq / p.pack;
     p.plan.tpb = C::NQT * p.tq;
     p.plan.workers = ctas;
+    p.plan.n_lo = few + 1;
     p.box_rows = box_rows(p.page, C::BC);
     p.slot_first = p.slot_stride < p.head_stride ? 1 : 0;
     kv.box[p.slot_first ? 0 : 1] = p.box_rows;
     constexpr int rows = C::NQT * kBlockQ;
-    p.o_part = static_cast<float *>(workspace);
-    p.lse_part = reinterpret_cast<float *>(static_cast<char *>(workspace) + part_o_bytes(ctas, rows, C::D));
+    char *const ws = workspace + part_bytes(kMaxRowWorkers, kRowRows, C::D) + job_bytes(kMaxRowWorkers);
+    p.o_part = reinterpret_cast<float *>(ws);
+    p.lse_part = reinterpret_cast<float *>(ws + part_o_bytes(ctas, rows, C::D));
+    p.jobs = reinterpret_cast<MergeJob *>(ws + part_bytes(ctas, rows, C::D));
+    p.cuts = reinterpret_cast<long long *>(ws + part_bytes(ctas, rows, C::D) + job_bytes(ctas));
     CUtensorMap mq, mk, mv;
-    int rc;
     const int elem = C::F16 ? 1 : 0;
     if ((rc = encode_view(&mq, q.base, C::D, q.dims, q.strides, C::CW, q.box, elem)) != FA_OK) return rc;
     if ((rc = encode_view(&mk, kv.base, C::D, kv.dims, kv.strides, C::CW, kv.box, elem)) != FA_OK) return rc;
     if ((rc = encode_view(&mv, v, C::D, kv.dims, kv.strides, C::CW, kv.box, elem)) != FA_OK) return rc;
-    fa_paged_tiles_kernel<C><<<unsigned(ctas), C::THREADS, C::SMEM_BYTES, st>>>(mq, mk, mv, p);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-    if (ctas < 2) return FA_OK;
-    return launch_after(fa_paged_merge_kernel<C::D, C::F16, rows, kBlockQ, C::BC>, dim3(unsigned(ctas - 1), rows / 16), 128,
-                        static_cast<const PagedParams &>(p), st);
+    PagedParams pf = base;
+    pf.plan.n_hi = few;
+    pf.say = 0;
+    if (few > 0 && (rc = launch_rows<RowCfg<C::D, C::F16>>(pf, workspace, ctas, dev, st)) != FA_OK) return rc;
+    if (few > 0) {   // beside the kernel before it, which began when the inputs were complete
+        rc = launch_after(fa_paged_tiles_kernel<C>, unsigned(ctas), C::THREADS, C::SMEM_BYTES, st, mq, mk, mv, p);
+        if (rc != FA_OK) return rc;
+    } else {
+        fa_paged_tiles_kernel<C><<<unsigned(ctas), C::THREADS, C::SMEM_BYTES, st>>>(mq, mk, mv, p);
+        if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    }
+    const int blocks = (ctas - 1) * (rows / 32) + (few > 0 ? pf.plan.workers - 1 : 0);
+    if (blocks == 0) return FA_OK;
+    return launch_after(fa_paged_merge_kernel<C>, unsigned(blocks), 256, 0, st, p, pf);
 }
 
 template <bool F16>
-int dispatch_tiles(PagedParams p, int d, int num_blocks, int Hkv, void *workspace, int ctas, int dev, cudaStream_t st) {
+int dispatch_tiles(PagedParams p, int d, int num_blocks, int Hkv, int few, char *workspace, int ctas, int dev, cudaStream_t st) {
     p.pack = largest_divisor(p.n_rep, kBlockQ);
     const View q{p.q, {p.Hq, p.plan.T, 1}, {d, p.q_stride, p.q_stride * p.plan.T}, {p.pack, kBlockQ / p.pack, 1}};
     View kv{p.k, {Hkv, p.page, num_blocks}, {p.head_stride, p.slot_stride, p.block_stride}, {1, 1, 1}};
@@ -154,26 +176,26 @@ int dispatch_tiles(PagedParams p, int d, int num_blocks, int Hkv, void *workspac
         std::swap(kv.strides[0], kv.strides[1]);
     }
     switch (d) {
-        case 32: return launch_tiles<Tile32<F16>>(p, q, kv, p.v, workspace, ctas, dev, st);
-        case 64: return launch_tiles<Tile64<F16>>(p, q, kv, p.v, workspace, ctas, dev, st);
-        case 80: return launch_tiles<Tile80<F16>>(p, q, kv, p.v, workspace, ctas, dev, st);
-        case 96: return launch_tiles<Tile96<F16>>(p, q, kv, p.v, workspace, ctas, dev, st);
-        case 128: return launch_tiles<Tile128<F16>>(p, q, kv, p.v, workspace, ctas, dev, st);
-        case 192: return launch_tiles<Tile192<F16>>(p, q, kv, p.v, workspace, ctas, dev, st);
-        default: return launch_tiles<Tile256<F16>>(p, q, kv, p.v, workspace, ctas, dev, st);
+        case 32: return launch_tiles<Tile32<F16>>(p, q, kv, p.v, few, workspace, ctas, dev, st);
+        case 64: return launch_tiles<Tile64<F16>>(p, q, kv, p.v, few, workspace, ctas, dev, st);
+        case 80: return launch_tiles<Tile80<F16>>(p, q, kv, p.v, few, workspace, ctas, dev, st);
+        case 96: return launch_tiles<Tile96<F16>>(p, q, kv, p.v, few, workspace, ctas, dev, st);
+        case 128: return launch_tiles<Tile128<F16>>(p, q, kv, p.v, few, workspace, ctas, dev, st);
+        case 192: return launch_tiles<Tile192<F16>>(p, q, kv, p.v, few, workspace, ctas, dev, st);
+        default: return launch_tiles<Tile256<F16>>(p, q, kv, p.v, few, workspace, ctas, dev, st);
     }
 }
 
 template <bool F16>
-int dispatch_rows(const PagedParams &p, int d, void *workspace, int ctas, int dev, cudaStream_t st) {
+int dispatch_rows(const PagedParams &p, int d, char *workspace, int ctas, int dev, cudaStream_t st) {
     switch (d) {
-        case 32: return launch_rows<RowCfg<32, F16>>(p, workspace, ctas, dev, st);
-        case 64: return launch_rows<RowCfg<64, F16>>(p, workspace, ctas, dev, st);
-        case 80: return launch_rows<RowCfg<80, F16>>(p, workspace, ctas, dev, st);
-        case 96: return launch_rows<RowCfg<96, F16>>(p, workspace, ctas, dev, st);
-        case 128: return launch_rows<RowCfg<128, F16>>(p, workspace, ctas, dev, st);
-        case 192: return launch_rows<RowCfg<192, F16>>(p, workspace, ctas, dev, st);
-        default: return launch_rows<RowCfg<256, F16>>(p, workspace, ctas, dev, st);
+        case 32: return launch_rows_only<32, F16>(p, workspace, ctas, dev, st);
+        case 64: return launch_rows_only<64, F16>(p, workspace, ctas, dev, st);
+        case 80: return launch_rows_only<80, F16>(p, workspace, ctas, dev, st);
+        case 96: return launch_rows_only<96, F16>(p, workspace, ctas, dev, st);
+        case 128: return launch_rows_only<128, F16>(p, workspace, ctas, dev, st);
+        case 192: return launch_rows_only<192, F16>(p, workspace, ctas, dev, st);
+        default: return launch_rows_only<256, F16>(p, workspace, ctas, dev, st);
     }
 }
 
@@ -237,13 +259,19 @@ int paged_fwd(const void *q, long long q_stride, const fa_paged_cache *cache, co
     p.scale_log2 = scale * 1.4426950408889634f;
     const int ctas = std::min(dev->num_sms, kMaxPagedCtas);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    p.plan.n_lo = 1;
+    p.plan.n_hi = max_new;
+    p.say = 1;
+    char *const ws = static_cast<char *>(workspace);
     // Row tiles of 128 need pages of whole swizzle atoms (8 slots); any other page, and calls of few rows,
-    // take the kernel that gathers key by key.
-    const bool tiles = (long long)max_new * p.n_rep > kRowRows && p.page % 8 == 0 && p.num_blocks > 0;
-    if (tiles)
-        return f16 ? dispatch_tiles<true>(p, d, p.num_blocks, Hkv, workspace, ctas, dev_id, st)
-                   : dispatch_tiles<false>(p, d, p.num_blocks, Hkv, workspace, ctas, dev_id, st);
-    return f16 ? dispatch_rows<true>(p, d, workspace, ctas, dev_id, st) : dispatch_rows<false>(p, d, workspace, ctas, dev_id, st);
+    // take the kernel that gathers key by key.  In a mixed call the requests of few rows take it too.
+    const int few = kRowRows / p.n_rep;   // new tokens whose rows fit it
+    if (max_new > few && p.page % 8 == 0 && p.num_blocks > 0) {
+        const int split = R > 1 ? few : 0;
+        return f16 ? dispatch_tiles<true>(p, d, p.num_blocks, Hkv, split, ws, ctas, dev_id, st)
+                   : dispatch_tiles<false>(p, d, p.num_blocks, Hkv, split, ws, ctas, dev_id, st);
+    }
+    return f16 ? dispatch_rows<true>(p, d, ws, ctas, dev_id, st) : dispatch_rows<false>(p, d, ws, ctas, dev_id, st);
 }
 
 }  // namespace
@@ -252,7 +280,9 @@ extern "C" {
 
 size_t fa_paged_workspace_bytes(int Hq, int Hkv, int d) {
     if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || fa_tile_config(d, nullptr, nullptr, nullptr, nullptr) != FA_OK) return 0;
-    return std::max(part_bytes(kMaxRowWorkers, kRowRows, d), part_bytes(kMaxPagedCtas, d == 256 ? kBlockQ : 2 * kBlockQ, d));
+    return part_bytes(kMaxRowWorkers, kRowRows, d) + job_bytes(kMaxRowWorkers) +
+           part_bytes(kMaxPagedCtas, d == 256 ? kBlockQ : 2 * kBlockQ, d) + job_bytes(kMaxPagedCtas) +
+           align256((kMaxPagedCtas + 1) * sizeof(long long));
 }
 
 int fa_paged_fwd(const void *q, long long q_stride, const fa_paged_cache *cache, const int *block_table,

@@ -29,6 +29,7 @@ struct PlanParams {
     int *status;
     long long max_len;             // max_blocks * page_size
     int R, T, max_new;
+    int n_lo, n_hi;                // requests of n_lo .. n_hi new tokens take part
     int causal, window;
     int groups;                    // head groups a request: Hq / pack
     int tpb;                       // new tokens a unit
@@ -39,23 +40,31 @@ struct Request {
     int q0, n, L;
 };
 
+// Quotient of values >= 0; 32-bit ones (nearly always) take the short division.
+FA_PLAN long long div_pos(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return (long long)((unsigned)a / (unsigned)b);
+    return a / b;
+}
+
 // sum_{i < n} floor((a i + b) / m), a, b >= 0, m >= 1.
 FA_PLAN long long floor_sum(long long n, long long m, long long a, long long b) {
     long long sum = 0;
     while (n > 0) {
         if (a >= m) {
-            sum += (n - 1) * n / 2 * (a / m);
-            a %= m;
+            const long long q = div_pos(a, m);
+            sum += (n - 1) * n / 2 * q;
+            a -= q * m;
         }
         if (b >= m) {
-            sum += n * (b / m);
-            b %= m;
+            const long long q = div_pos(b, m);
+            sum += n * q;
+            b -= q * m;
         }
         if (a == 0) break;
         const long long y = a * n + b;
         if (y < m) break;
-        n = y / m;
-        b = y % m;
+        n = div_pos(y, m);
+        b = y - n * m;
         const long long t = m;
         m = a;
         a = t;
@@ -66,7 +75,7 @@ FA_PLAN long long floor_sum(long long n, long long m, long long a, long long b) 
 // sum_{b < nb} floor(max(0, a b + c) / m).
 FA_PLAN long long floor_sum_from(long long nb, long long m, long long a, long long c) {
     if (c < 0) {
-        const long long skip = (-c + a - 1) / a;   // blocks whose value is below 0
+        const long long skip = div_pos(-c + a - 1, a);   // blocks whose value is below 0
         if (skip >= nb) return 0;
         nb -= skip;
         c += skip * a;
@@ -86,6 +95,7 @@ FA_PLAN Request load_request(const PlanParams &p, int r, bool say = false) {
 #endif
         q.n = 0;
     }
+    if (q.n < p.n_lo || q.n > p.n_hi) q.n = 0;
     return q;
 }
 
@@ -120,23 +130,21 @@ FA_PLAN long long plan_steps(const PlanParams &p, const Request &q, int nb) {
     return s;
 }
 
-// What the block knows of the whole line: total steps, and the sums before each thread's segment.
+FA_PLAN int plan_units(const PlanParams &p, const Request &q) { return p.groups * plan_blocks(p, q); }
+
+// What a block knows of the whole line: the steps and the units before each thread's segment of
+// requests (segment t: requests [t seg, (t + 1) seg), seg = ceil(R / NT)).
 template <int NT_>
 struct PlanScan {
     static constexpr int NT = NT_;   // threads that take part = segments
     long long seg_start[NT + 1];
     long long warp_sum[NT / 32];
+    int seg_units[NT + 1];
 };
 
-// By all NT threads of the block.  Returns the total.
-template <int KS, int NT>
-__device__ inline long long plan_scan(const PlanParams &p, PlanScan<NT> &sh, int tid, bool say) {
-    const int seg = (p.R + NT - 1) / NT;
-    long long mine = 0;
-    for (int r = tid * seg; r < min(p.R, (tid + 1) * seg); ++r) {
-        const Request q = load_request(p, r, say);
-        if (q.n > 0) mine += p.groups * plan_steps<KS>(p, q, plan_blocks(p, q));
-    }
+// Sum of the values of the threads before this one, over all NT threads of the block.
+template <int NT>
+__device__ inline long long block_before(long long mine, long long *warp_sum, int tid, long long &total) {
     const int lane = tid % 32, warp = tid / 32;
     long long upto = mine;
 #pragma unroll
@@ -144,31 +152,59 @@ __device__ inline long long plan_scan(const PlanParams &p, PlanScan<NT> &sh, int
         const long long y = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += y;
     }
-    if (lane == 31) sh.warp_sum[warp] = upto;
+    __syncthreads();   // the last use of warp_sum is over
+    if (lane == 31) warp_sum[warp] = upto;
     __syncthreads();
-    long long before = 0, total = 0;
+    long long before = 0;
+    total = 0;
 #pragma unroll
     for (int w = 0; w < NT / 32; ++w) {
-        const long long s = sh.warp_sum[w];
+        const long long s = warp_sum[w];
         if (w < warp) before += s;
         total += s;
     }
-    sh.seg_start[tid] = before + upto - mine;
-    if (tid == 0) sh.seg_start[NT] = total;
+    return before + upto - mine;
+}
+
+// By all NT threads of the block.  Returns the total.
+template <int KS, int NT>
+__device__ inline long long plan_scan(const PlanParams &p, PlanScan<NT> &sh, int tid, bool say) {
+    const int seg = (p.R + NT - 1) / NT;
+    long long steps = 0, units = 0, total, total_units;
+    for (int r = tid * seg; r < min(p.R, (tid + 1) * seg); ++r) {
+        const Request q = load_request(p, r, say);
+        if (q.n > 0) {
+            steps += p.groups * plan_steps<KS>(p, q, plan_blocks(p, q));
+            units += plan_units(p, q);
+        }
+    }
+    sh.seg_start[tid] = block_before<NT>(steps, sh.warp_sum, tid, total);
+    sh.seg_units[tid] = int(block_before<NT>(units, sh.warp_sum, tid, total_units));
+    if (tid == 0) {
+        sh.seg_start[NT] = total;
+        sh.seg_units[NT] = int(total_units);
+    }
     __syncthreads();
     return total;
 }
 
 // First step of worker w's range, and the worker that step x belongs to.
 FA_PLAN long long range_start(long long total, int workers, int w) {
-    const long long q = total / workers, rem = total % workers;
+    const long long q = div_pos(total, workers), rem = total - q * workers;
     return w * q + min((long long)w, rem);
 }
 FA_PLAN int range_owner(long long total, int workers, long long x) {
-    const long long q = total / workers, rem = total % workers;
-    if (x < rem * (q + 1)) return int(x / (q + 1));
-    return int(rem + (x - rem * (q + 1)) / q);
+    const long long q = div_pos(total, workers), rem = total - q * workers;
+    if (x < rem * (q + 1)) return int(div_pos(x, q + 1));
+    return int(rem + div_pos(x - rem * (q + 1), q));
 }
+
+// What the merge is told of one cut: the unit that it crosses first (parts = 0: none), its pieces
+// and its rows.  Piece 0 is in slot `first_slot`, piece s > 0 in slot 2 (w - 1 + s) for cut w.
+struct MergeJob {
+    int parts, first_slot;
+    int row0, tokens, g;       // first row of q, tokens, head group
+};
 
 // A unit on the line: its place, and where on the line it begins and ends.
 struct Unit {
@@ -196,7 +232,7 @@ FA_PLAN Unit plan_find(const PlanParams &p, const PlanScan<NT> &sh, long long x)
         if (x < at + group * p.groups) break;
         at += group * p.groups;
     }
-    u.g = int((x - at) / group);
+    u.g = int(div_pos(x - at, group));
     at += u.g * group;
     int b_lo = 0, b_hi = plan_blocks(p, u.q);
     while (b_hi - b_lo > 1) {
@@ -206,6 +242,31 @@ FA_PLAN Unit plan_find(const PlanParams &p, const PlanScan<NT> &sh, long long x)
     }
     u.b = b_lo;
     u.begin = at + plan_steps<KS>(p, u.q, b_lo);
+    plan_range<KS>(p, u.q, u.b, u.js, u.je);
+    return u;
+}
+
+// Unit number k (0 <= k < units) of the line, without its place on it (begin = 0); `units_before` are
+// the units before each of `segments` segments of `seg` requests.
+template <int KS>
+FA_PLAN Unit plan_unit(const PlanParams &p, const int *units_before, int segments, int seg, int k) {
+    int lo = 0, hi = segments;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (units_before[mid] <= k) lo = mid;
+        else hi = mid;
+    }
+    Unit u{};
+    int at = units_before[lo];
+    for (u.r = lo * seg; u.r < p.R; ++u.r) {
+        u.q = load_request(p, u.r);
+        const int n = u.q.n > 0 ? plan_units(p, u.q) : 0;
+        if (k < at + n) break;
+        at += n;
+    }
+    const int nb = plan_blocks(p, u.q);
+    u.g = (k - at) / nb;
+    u.b = k - at - u.g * nb;
     plan_range<KS>(p, u.q, u.b, u.js, u.je);
     return u;
 }
@@ -225,6 +286,54 @@ FA_PLAN void plan_next(const PlanParams &p, Unit &u) {
         }
     }
     plan_range<KS>(p, u.q, u.b, u.js, u.je);
+}
+
+// The schedule of the CTAs of a tile kernel, in two phases.  First whole units, CTA c units c,
+// c + G, c + 2 G, ...: CTAs that run at the same time have neighbouring units, the token blocks of one
+// head, and go through its keys side by side, so that K and V come from L2.  As many rounds of G units
+// as leave every CTA within its equal share of the steps; then the rest of the line is cut, each
+// CTA taking what its share still lacks: CTA c the steps cuts[c] .. cuts[c + 1] - 1.
+// By all NT >= G threads; `cuts` is shared memory for G + 1 places.  Returns the rounds.
+template <int KS, int NT>
+__device__ inline int plan_schedule(const PlanParams &p, PlanScan<NT> &sh, long long total, long long *cuts, int tid) {
+    const int G = p.workers, units = sh.seg_units[NT], seg = (p.R + NT - 1) / NT;
+    const long long share = tid < G ? range_start(total, G, tid + 1) - range_start(total, G, tid) : 0;
+    long long mine = 0;
+    int rounds = 0;
+    for (;; ++rounds) {
+        int len = 0;
+        bool stop = false;
+        if (tid < G) {
+            const long long k = (long long)rounds * G + tid;
+            stop = k >= units;
+            if (!stop) {
+                const Unit u = plan_unit<KS>(p, sh.seg_units, NT, seg, int(k));
+                len = u.je - u.js;
+                stop = mine + len > share;
+            }
+        }
+        if (__syncthreads_or(stop)) break;
+        mine += len;
+    }
+    long long rest;
+    const long long before = block_before<NT>(share - mine, sh.warp_sum, tid, rest);
+    if (tid < G) cuts[tid] = total - rest + before;
+    if (tid == 0) cuts[G] = total;
+    __syncthreads();
+    return rounds;
+}
+
+// The merge job of cut w, which lies at `cut` in unit u, where the worker before begins at `before` and
+// the unit's last step is done by worker `last`.
+FA_PLAN MergeJob merge_job(const PlanParams &p, const Unit &u, int w, long long before, long long cut, int last) {
+    MergeJob j{};
+    if (before == cut || u.begin >= cut || before > u.begin) return j;
+    j.parts = last - (w - 1) + 1;
+    j.first_slot = 2 * (w - 1) + (before == u.begin ? 0 : 1);
+    j.row0 = u.q.q0 + u.b * p.tpb;
+    j.tokens = min(u.q.n - u.b * p.tpb, p.tpb);
+    j.g = u.g;
+    return j;
 }
 
 #undef FA_PLAN

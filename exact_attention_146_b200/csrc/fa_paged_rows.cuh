@@ -37,6 +37,8 @@ struct PagedParams {
     float *o_part, *lse_part;      // workspace: [workers][2][rows][d], [workers][2][rows]
     int Hq, pack, n_rep, page, num_blocks;
     float scale_log2;              // scale * log2(e)
+    int say;                       // this kernel reports requests that are out of range
+    MergeJob *jobs;                // workspace: [workers], the job of each cut
 };
 
 constexpr int kRowKeys = 16;       // keys a step
@@ -130,17 +132,27 @@ __global__ void __launch_bounds__(C::THREADS, 1) fa_paged_rows_kernel(const __gr
     __shared__ PlanScan<C::THREADS> scan;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge may be set up meanwhile
     const int lane = int(threadIdx.x) % 32, warp = int(threadIdx.x) / 32;
-    const long long total = plan_scan<kRowKeys>(p.plan, scan, int(threadIdx.x), blockIdx.x == 0);
+    const long long total = plan_scan<kRowKeys>(p.plan, scan, int(threadIdx.x), blockIdx.x == 0 && p.say != 0);
     const int worker = int(blockIdx.x) * C::WARPS + warp;
     const long long x0 = range_start(total, p.plan.workers, worker);
     const long long x1 = range_start(total, p.plan.workers, worker + 1);
-    if (x0 >= x1) return;
+    if (x0 >= x1) {
+        if (lane == 0) p.jobs[worker].parts = 0;
+        return;
+    }
 
     Cursor load;
     load.u = plan_find<kRowKeys>(p.plan, scan, x0);
     load.j = load.u.js + int(x0 - load.u.begin);
     load.left = int(min(x1 - x0, 0x7fffffffLL));
     Cursor cur = load;
+    if (lane == 0) {
+        MergeJob job{};
+        if (worker > 0 && load.u.begin < x0)
+            job = merge_job(p.plan, load.u, worker, range_start(total, p.plan.workers, worker - 1), x0,
+                            range_owner(total, p.plan.workers, load.u.begin + (load.u.je - load.u.js) - 1));
+        p.jobs[worker] = job;
+    }
 
     const uint32_t base = sm100::smem_u32(ring) + uint32_t(warp * C::STAGES * C::STAGE);
 
@@ -337,71 +349,100 @@ __global__ void __launch_bounds__(C::THREADS, 1) fa_paged_rows_kernel(const __gr
     cp_async_wait<0>();
 }
 
-// Merges the pieces of every unit that a cut crosses: one block a cut, the first cut in a unit
-// does it.  ROWS: rows a unit has in the workspace, in tiles of TILE (each TILE / pack tokens of
-// `pack` heads); KS: keys a step; the block's warps take rows blockIdx.y * ROWS / gridDim.y ....
-template <int D, bool F16, int ROWS, int TILE, int KS>
-__global__ void __launch_bounds__(128) fa_paged_merge_kernel(const __grid_constant__ PagedParams p) {
-    __shared__ PlanScan<128> scan;
-    const long long total = plan_scan<KS>(p.plan, scan, int(threadIdx.x), false);
-    const int w = int(blockIdx.x) + 1;
-    const long long cut = range_start(total, p.plan.workers, w), before = range_start(total, p.plan.workers, w - 1);
-    bool mine = cut < total;
-    Unit u{};
-    if (mine) {
-        u = plan_find<KS>(p.plan, scan, cut);
-        mine = u.begin < cut && before <= u.begin;
-    }
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // the pieces are written
-    if (!mine) return;
-    const int w_last = range_owner(total, p.plan.workers, u.begin + (u.je - u.js) - 1);
-    const int first_slot = 2 * (w - 1) + (before == u.begin ? 0 : 1), parts = w_last - (w - 1) + 1;
-    const int lane = int(threadIdx.x) % 32;
-    const int per_y = ROWS / int(gridDim.y);
-    for (int row = int(blockIdx.y) * per_y + int(threadIdx.x) / 32; row < (int(blockIdx.y) + 1) * per_y; row += 4) {
+// Merges the pieces of the unit that cut w crosses first: rows [row0, row1) of it, a warp each in turn.
+// ROWS: rows a unit has in the workspace, in tiles of TILE (each TILE / pack tokens of `pack` heads).
+// there(s): whether worker w - 1 + s did any steps.  All pieces' rows are loaded eight at a time.
+template <int D, bool F16, int ROWS, int TILE, class There>
+__device__ __forceinline__ void merge_unit(const PagedParams &p, int w, int row0, int row1, const There &there) {
+    const MergeJob job = p.jobs[w];
+    if (job.parts == 0) return;
+    constexpr int VEC = D % 128 == 0 ? 4 : (D % 64 == 0 ? 2 : 1), PER = (D + 32 * VEC - 1) / (32 * VEC);
+    const int lane = int(threadIdx.x) % 32, warps = int(blockDim.x) / 32;
+    auto row_of = [&](int s, int row) { return (long long)(s == 0 ? job.first_slot : 2 * (w - 1 + s)) * ROWS + row; };
+    for (int row = row0 + int(threadIdx.x) / 32; row < row1; row += warps) {
         const int tile = row / TILE, in_tile = row - tile * TILE, i = in_tile / p.pack, tq = TILE / p.pack;
-        const int token = u.b * p.plan.tpb + tile * tq + i, head = u.g * p.pack + in_tile - i * p.pack;
-        if (i >= tq || token >= u.q.n) continue;
-        auto slot_of = [&](int part) { return part == 0 ? first_slot : 2 * (w - 1 + part); };
-        float m = -INFINITY;
-        for (int s = lane; s < parts; s += 32) m = fmaxf(m, p.lse_part[(long long)slot_of(s) * ROWS + row]);
+        const int token = tile * tq + i, head = job.g * p.pack + in_tile - i * p.pack;
+        if (i >= tq || token >= job.tokens) continue;
+        float m = -INFINITY, sum = 0.f;
+        float acc[PER][VEC] = {};
+        for (int base = 0; base < job.parts; base += 32) {   // 32 pieces at a time, as the online softmax
+            const int s = base + lane;
+            const float ls = s < job.parts && there(s) ? p.lse_part[row_of(s, row)] : -INFINITY;
+            float mx = ls;
 #pragma unroll
-        for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        constexpr int PER = (D + 31) / 32;
-        float acc[PER] = {};
-        float sum = 0.f;
-        if (m != -INFINITY) {
-            for (int base = 0; base < parts; base += 32) {
-                const int s = base + lane;
-                const float ls = s < parts ? p.lse_part[(long long)slot_of(s) * ROWS + row] : -INFINITY;
-                const float wl = ls == -INFINITY ? 0.f : __expf(ls - m);
-                sum += wl;
-                const int n = min(32, parts - base);
-#pragma unroll 4
-                for (int t = 0; t < n; ++t) {
-                    const float wt = __shfl_sync(0xffffffffu, wl, t);
-                    const float *src = p.o_part + ((long long)slot_of(base + t) * ROWS + row) * D;
+            for (int o = 16; o > 0; o /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const float now = fmaxf(m, mx);
+            if (now == -INFINITY) continue;
+            const float wl = __expf(ls - now), keep = __expf(m - now);
+            m = now;
+            float add = wl;
+#pragma unroll
+            for (int o = 16; o > 0; o /= 2) add += __shfl_xor_sync(0xffffffffu, add, o);
+            sum = sum * keep + add;
+#pragma unroll
+            for (int e = 0; e < PER; ++e)
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) acc[e][v] *= keep;
+            const int n = min(32, job.parts - base);
+            for (int t0 = 0; t0 < n; t0 += 8) {
+                float x[8][PER][VEC];
+                float wt[8];
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    wt[t] = __shfl_sync(0xffffffffu, wl, (t0 + t) % 32);
+                    const bool use = t0 + t < n && wt[t] != 0.f;   // a piece of weight 0 may not have been written
+#pragma unroll
+                    for (int e = 0; e < PER; ++e) {
+                        const int col = (e * 32 + lane) * VEC;
+                        const float *src = p.o_part + row_of(base + t0 + t, row) * D + col;
+#pragma unroll
+                        for (int v = 0; v < VEC; ++v) x[t][e][v] = 0.f;
+                        if (use && col < D) {
+                            if constexpr (VEC == 4) {
+                                const float4 f = *reinterpret_cast<const float4 *>(src);
+                                x[t][e][0] = f.x, x[t][e][1] = f.y, x[t][e][2] = f.z, x[t][e][3] = f.w;
+                            } else if constexpr (VEC == 2) {
+                                const float2 f = *reinterpret_cast<const float2 *>(src);
+                                x[t][e][0] = f.x, x[t][e][1] = f.y;
+                            } else {
+                                x[t][e][0] = *src;
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
 #pragma unroll
                     for (int e = 0; e < PER; ++e)
-                        if (lane + 32 * e < D) acc[e] = fmaf(wt, src[lane + 32 * e], acc[e]);
-                }
-            }
 #pragma unroll
-            for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                        for (int v = 0; v < VEC; ++v) acc[e][v] = fmaf(wt[t], x[t][e][v], acc[e][v]);
+            }
         }
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        const long long at = u.q.q0 + token;
+        const long long at = job.row0 + token;
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
-            const int col = lane + 32 * e;
-            if (col < D) {
-                const float x = acc[e] * inv;
-                p.out[(at * p.Hq + head) * D + col] =
-                    F16 ? __half_as_ushort(__float2half_rn(x)) : __bfloat16_as_ushort(__float2bfloat16_rn(x));
+            const int col = (e * 32 + lane) * VEC;
+            if (col >= D) continue;
+            uint16_t *dst = p.out + (at * p.Hq + head) * D + col;
+            if constexpr (VEC == 1) {
+                const float x = acc[e][0] * inv;
+                *dst = F16 ? __half_as_ushort(__float2half_rn(x)) : __bfloat16_as_ushort(__float2bfloat16_rn(x));
+            } else {
+#pragma unroll
+                for (int v = 0; v < VEC; v += 2)
+                    *reinterpret_cast<uint32_t *>(dst + v) = sm100::pack_x2<F16>(acc[e][v] * inv, acc[e][v + 1] * inv);
             }
         }
         if (p.lse != nullptr && lane == 0) p.lse[(long long)head * p.plan.T + at] = sum > 0.f ? m + logf(sum) : -INFINITY;
     }
+}
+
+// The merge of a call that has pieces of few rows only: one block a cut.
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) fa_paged_merge_rows_kernel(const __grid_constant__ PagedParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the pieces and jobs are written
+    merge_unit<D, F16, kRowRows, kRowRows>(p, int(blockIdx.x) + 1, 0, kRowRows, [](int) { return true; });
 }
 
 }  // namespace fa

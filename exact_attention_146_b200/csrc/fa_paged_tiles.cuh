@@ -5,9 +5,9 @@
 // different from the dense forward:
 //   * a row tile stacks `pack` query heads of one KV head over 128 / pack tokens (flat row
 //     token * pack + head), so a short chunk still fills it, and the heads share every K/V load;
-//   * the work is one line of key-tile steps cut evenly over the CTAs (fa_paged_plan.cuh): a single
-//     long request keeps every SM busy to the end.  A CTA cuts at most two units, their pieces go to
-//     the workspace and the merge kernel combines them;
+//   * every CTA gets the same number of key-tile steps (plan_schedule): whole units first, then a range of
+//     the rest of the line, so that a single long request keeps every SM busy to the end.  A range
+//     ends inside at most two units; their pieces go to the workspace and the merge kernel combines them;
 //   * K and V tiles are put together from the largest power-of-two runs of slots that divide a page
 //     (8 rows at least: one swizzle atom), one TMA box each; runs that no row of the unit sees take a
 //     block index past the cache and are filled with zeros by the copy engine.  Slots of the last run
@@ -24,67 +24,68 @@ struct PagedTileParams : PagedParams {
     int tq;            // tokens a row tile: 128 / pack
     int box_rows;      // slots a K/V box
     int slot_first;    // the tensor map's second axis is the slot (else the head)
+    long long *cuts;   // workspace: [workers + 1] the cuts of the line, for the merge
 };
 
-// A unit as one CTA does it: its key tiles clipped to the CTA's range.
+// The units before each of 64 segments of the requests: what the planner needs to find whole units.
+constexpr int kCoarse = 64;
+constexpr int kQueue = 4;   // units planned ahead
+
+// A unit as one CTA does it, made by the planner warp for the other roles.
 struct PagedUnit {
-    Unit u;
-    int js[2], je[2], j_lo, j_hi;   // as UnitInfo
-    bool whole;                     // the unit lies wholly in this range
-    int slot;                       // else: where in the workspace its piece goes
+    int js[2], je[2];          // key tiles each row tile visits here (empty: js == je)
+    int j_lo, j_hi;            // their union
+    int row0, tokens;          // first row of q, new tokens (both row tiles); tokens < 0: no more units
+    int pos0;                  // position of the first token: its last visible key if causal
+    int L, r, g;               // keys of the request, the request, the head group
+    int lo, hi;                // keys that some row sees
+    int slot;                  // the piece's place in the workspace; -1: the whole unit is done here
+    int pad;
 };
 
+// Shared memory between the pipeline's barriers and the staging: the queue's barriers (full, empty),
+// its entries, and the coarse counts.
 template <class C>
+struct PlanSmem {
+    static constexpr int BARS = C::SMEM_MISC + 16;
+    static constexpr int UNITS = BARS + 2 * kQueue * 8;
+    static constexpr int COARSE = UNITS + kQueue * int(sizeof(PagedUnit));
+    static_assert(COARSE + (kCoarse + 1) * 4 <= C::SMEM_OST, "the plan lies before the staging");
+    static_assert(BARS % 8 == 0 && sizeof(PagedUnit) == 64, "alignment");
+    // who hands an entry back: the TMA warp, the MMA warp and each softmax warp
+    static constexpr int READERS = 2 + C::SOFTMAX_WARPS;
+};
+constexpr int kSiteUnitFull = 14, kSiteUnitEmpty = 15;   // waits of the queue (bits 8..15 of the status word)
+
+// A role's end of the queue.
+template <class C, int ROLE>
 struct PagedUnits {
     using Unit = PagedUnit;
-    const PagedTileParams &p;
-    Cursor at;                      // the next piece
-    bool first;                     // it begins where the range does
+    uint32_t sbase;
+    uint8_t *smem;
+    const Ctl &ctl;
+    int box_rows;
+    uint32_t n;
 
     __device__ __forceinline__ bool next(PagedUnit &w) {
-        if (at.left <= 0) return false;
-        const int pjs = at.j, pje = min(at.u.je, at.j + at.left);
-        w.u = at.u;
-        w.whole = pjs == at.u.js && pje == at.u.je;
-        w.slot = 2 * int(blockIdx.x) + (first ? 0 : 1);
-        const long long diag = (long long)w.u.q.L - w.u.q.n;
-        w.j_lo = 0x7fffffff;
-        w.j_hi = 0;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            int js = 0, je = 0;
-            const int tok0 = w.u.b * p.plan.tpb + t * p.tq, tok1 = min(w.u.q.n, tok0 + p.tq);
-            if (t < C::NQT && tok0 < tok1) {
-                const long long last = p.plan.causal ? tok1 - 1 + diag : (long long)w.u.q.L - 1;
-                const long long from = p.plan.window > 0 ? tok0 + diag - p.plan.window + 1 : 0;
-                js = max(int(max(from, 0LL) / C::BC), pjs);
-                je = min(int(max(last, 0LL) / C::BC) + 1, pje);
-                if (je <= js) js = je = 0;
-            }
-            w.js[t] = js;
-            w.je[t] = je;
-            if (je > js) {
-                w.j_lo = min(w.j_lo, js);
-                w.j_hi = max(w.j_hi, je);
-            }
-        }
-        if (w.j_hi == 0) w.j_lo = 0;
-        at.left -= pje - pjs;
-        first = false;
-        if (at.left > 0) {
-            plan_next<C::BC>(p.plan, at.u);
-            at.j = at.u.js;
-        }
-        return true;
+        const int i = int(n % kQueue);
+        const uint32_t bars = sbase + PlanSmem<C>::BARS;
+        if (!warp_wait_bar<ROLE>(bars + 8u * i, (n / kQueue) & 1u, ctl, kSiteUnitFull)) return false;
+        w = *reinterpret_cast<const PagedUnit *>(smem + PlanSmem<C>::UNITS + i * int(sizeof(PagedUnit)));
+        __syncwarp();
+        if (threadIdx.x % 32 == 0) sm100::mbar_arrive(bars + 8u * (kQueue + i));
+        ++n;
+        return w.tokens >= 0;
     }
 
     // Rows of the V tile from the request's length to the end of the box that holds it.
     __device__ __forceinline__ void v_landed(const PagedUnit &w, int j, uint32_t tile) const {
-        const int a = w.u.q.L - j * C::BC;
-        if (a <= 0 || a >= C::BC || a % p.box_rows == 0) return;
-        const int b = (a / p.box_rows + 1) * p.box_rows;
-#pragma unroll
+        const int a = w.L - j * C::BC;
+        if (a <= 0 || a >= C::BC || a % box_rows == 0) return;
+        const int b = (a / box_rows + 1) * box_rows;
+#pragma unroll 1
         for (int c = 0; c < C::NCH; ++c)
+#pragma unroll 1
             for (int i = a * C::RB + int(threadIdx.x % 32) * 16; i < b * C::RB; i += 512)
                 sm100::st_shared_v4(tile + uint32_t(c * C::KV_CHUNK + i), 0u, 0u, 0u, 0u);
         sm100::fence_proxy_async_smem();   // the MMA reads through the async proxy
@@ -92,9 +93,77 @@ struct PagedUnits {
     }
 };
 
+// The planner: one thread walks this CTA's units (its whole ones, then its range of the line) and
+// queues them, so that the other roles do none of the plan's arithmetic.
+template <class C>
+__device__ void paged_plan_role(const PagedTileParams &p, const int *units_before, int seg, int whole_units, Cursor at,
+                                uint32_t sbase, uint8_t *smem, const Ctl &ctl) {
+    bool first = true;
+    int k = int(blockIdx.x);
+    const uint32_t bars = sbase + PlanSmem<C>::BARS;
+#pragma unroll 1
+    for (uint32_t n = 0;; ++n) {
+        PagedUnit w{};
+        w.tokens = -1;
+        Unit u{};
+        int pjs = 0, pje = 0;
+        if (k < whole_units) {
+            u = plan_unit<C::BC>(p.plan, units_before, kCoarse, seg, k);
+            pjs = u.js;
+            pje = u.je;
+            k += p.plan.workers;
+            w.slot = -1;
+            w.tokens = 0;
+        } else if (at.left > 0) {
+            u = at.u;
+            pjs = at.j;
+            pje = min(u.je, at.j + at.left);
+            w.slot = pjs == u.js && pje == u.je ? -1 : 2 * int(blockIdx.x) + (first ? 0 : 1);
+            w.tokens = 0;
+            first = false;
+            at.left -= pje - pjs;
+            if (at.left > 0) {
+                plan_next<C::BC>(p.plan, at.u);
+                at.j = at.u.js;
+            }
+        }
+        if (w.tokens == 0) {
+            const long long diag = (long long)u.q.L - u.q.n;
+            const int tok0 = u.b * p.plan.tpb;
+            w.row0 = u.q.q0 + tok0;
+            w.tokens = min(u.q.n - tok0, p.plan.tpb);
+            w.pos0 = int(tok0 + diag);
+            w.L = u.q.L;
+            w.r = u.r;
+            w.g = u.g;
+            unit_keys(p.plan, u, w.lo, w.hi);
+            w.j_lo = 0x7fffffff;
+#pragma unroll
+            for (int t = 0; t < C::NQT; ++t) {
+                const int t0 = t * p.tq, t1 = min(w.tokens, t0 + p.tq);
+                if (t0 >= t1) continue;
+                const int last = p.plan.causal ? w.pos0 + t1 - 1 : w.L - 1;
+                const int from = p.plan.window > 0 ? w.pos0 + t0 - p.plan.window + 1 : 0;
+                const int js = max(max(from, 0) / C::BC, pjs), je = min(max(last, 0) / C::BC + 1, pje);
+                if (je <= js) continue;
+                w.js[t] = js;
+                w.je[t] = je;
+                w.j_lo = min(w.j_lo, js);
+                w.j_hi = max(w.j_hi, je);
+            }
+            if (w.j_hi == 0) w.j_lo = 0;
+        }
+        const int i = int(n % kQueue);
+        if (!wait_bar<kRoleControl>(bars + 8u * (kQueue + i), ((n / kQueue) & 1u) ^ 1u, ctl, kSiteUnitEmpty)) return;
+        *reinterpret_cast<PagedUnit *>(smem + PlanSmem<C>::UNITS + i * int(sizeof(PagedUnit))) = w;
+        sm100::mbar_arrive(bars + 8u * i);
+        if (w.tokens < 0) return;
+    }
+}
+
 template <class C>
 __device__ void paged_producer_role(const CUtensorMap *tm_q, const CUtensorMap *tm_k, const CUtensorMap *tm_v,
-                                    const PagedTileParams &p, PagedUnits<C> units, uint32_t sbase, const Ctl &ctl) {
+                                    const PagedTileParams &p, PagedUnits<C, kRoleControl> units, uint32_t sbase, const Ctl &ctl) {
     auto bar = [&](int i) { return sbase + C::SMEM_BAR + 8u * uint32_t(i); };
     sm100::prefetch_tensormap(tm_q);
     sm100::prefetch_tensormap(tm_k);
@@ -108,6 +177,22 @@ __device__ void paged_producer_role(const CUtensorMap *tm_q, const CUtensorMap *
     PagedUnit w;
     while (ok && units.next(w)) {
         if (w.j_hi == w.j_lo) continue;
+        const int kvh = w.g * p.pack / p.n_rep;
+        const int *table = p.table + w.r * p.table_stride;
+        // Block and slot of box `lane` of key tile j (a block past the cache: zeros).
+        auto find_box = [&](int j, int &block, int &slot) {
+            const int key = j * C::BC + lane * p.box_rows;
+            const bool seen = lane < boxes && key <= w.hi && key + p.box_rows > w.lo;
+            const int page = seen ? key / p.page : 0;
+            slot = seen ? key - page * p.page : 0;
+            block = seen ? __ldg(table + page) : p.num_blocks;
+        };
+        auto slot_named = [&](int j) {   // the table was asked for this box
+            const int key = j * C::BC + lane * p.box_rows;
+            return lane < boxes && key <= w.hi && key + p.box_rows > w.lo;
+        };
+        int block, slot;
+        find_box(w.j_lo, block, slot);
 #pragma unroll
         for (int t = 0; t < C::NQT; ++t) {
             if (!ok || w.je[t] == w.js[t]) continue;
@@ -122,30 +207,16 @@ __device__ void paged_producer_role(const CUtensorMap *tm_q, const CUtensorMap *
             const uint32_t dst = sbase + C::SMEM_Q + (t * C::NQB + qb) * C::Q_TILE;
 #pragma unroll
             for (int c = 0; c < C::NCH; ++c)
-                sm100::tma_load_4d_elected(dst + c * C::Q_CHUNK, tm_q, fb, c * C::CW, w.u.g * p.pack,
-                                           w.u.q.q0 + w.u.b * p.plan.tpb + t * p.tq, 0);
+                sm100::tma_load_4d_elected(dst + c * C::Q_CHUNK, tm_q, fb, c * C::CW, w.g * p.pack, w.row0 + t * p.tq, 0);
         }
-        int lo, hi;
-        unit_keys(p.plan, w.u, lo, hi);
-        const int kvh = w.u.g * p.pack / p.n_rep;
-        // Block and slot of box `lane` of key tile j (a block past the cache: zeros).
-        auto find_box = [&](int j, int &block, int &slot) {
-            block = p.num_blocks;
-            slot = 0;
-            const int key = j * C::BC + lane * p.box_rows;
-            if (lane >= boxes || key > hi || key + p.box_rows <= lo) return;
-            const int page = key / p.page;
-            const int id = __ldg(p.table + w.u.r * p.table_stride + page);
-            slot = key - page * p.page;
-            if (id >= 0 && id < p.num_blocks) block = id;
-            else fa_host::report_range(p.plan.status, fa_host::kSiteTableId, w.u.r);
-        };
-        int block, slot;
-        find_box(w.j_lo, block, slot);
         for (int j = w.j_lo; ok && j < w.j_hi; ++j) {
             int next_block = 0, next_slot = 0;
             if (j + 1 < w.j_hi) find_box(j + 1, next_block, next_slot);   // looked up while this tile's slots are waited for
-#pragma unroll
+            if (block < 0 || block > p.num_blocks || (block == p.num_blocks && slot_named(j))) {
+                fa_host::report_range(p.plan.status, fa_host::kSiteTableId, w.r);
+                block = p.num_blocks;
+            }
+#pragma unroll 1
             for (int which = 0; which < 2; ++which) {
                 const int s = int(kv_cnt % C::NS);
                 if (!warp_wait_bar<kRoleControl>(bar(C::B_EMPTY + s), ((kv_cnt / C::NS) & 1u) ^ 1u, ctl, kSiteKvEmpty)) { ok = false; break; }
@@ -153,6 +224,7 @@ __device__ void paged_producer_role(const CUtensorMap *tm_q, const CUtensorMap *
                 sm100::mbar_arrive_expect_tx_elected(fb, C::KV_TILE);
                 const uint32_t dst = sbase + C::SMEM_KV + s * C::KV_TILE;
                 const CUtensorMap *m = which ? tm_v : tm_k;
+#pragma unroll 1
                 for (int i = 0; i < boxes; ++i) {
                     const int b = __shfl_sync(0xffffffffu, block, i), sl = __shfl_sync(0xffffffffu, slot, i);
                     const int c1 = p.slot_first ? sl : kvh, c2 = p.slot_first ? kvh : sl;
@@ -170,7 +242,7 @@ __device__ void paged_producer_role(const CUtensorMap *tm_q, const CUtensorMap *
 }
 
 template <class C>
-__device__ void paged_softmax_role(const PagedTileParams &p, PagedUnits<C> units, uint32_t sbase, uint32_t tmem, const Ctl &ctl,
+__device__ void paged_softmax_role(const PagedTileParams &p, PagedUnits<C, kRoleSoftmax> units, uint32_t sbase, uint32_t tmem, const Ctl &ctl,
                                    int warp, int lane) {
     auto bar = [&](int i) { return sbase + C::SMEM_BAR + 8u * uint32_t(i); };
     constexpr int D = C::D;
@@ -182,12 +254,11 @@ __device__ void paged_softmax_role(const PagedTileParams &p, PagedUnits<C> units
     PagedUnit w;
     while (units.next(w)) {
         const int js = w.js[t], je = w.je[t], nk = je - js;
-        const int tok0 = w.u.b * p.plan.tpb + t * p.tq, token = tok0 + i_tok;
-        const int diag = w.u.q.L - w.u.q.n;
+        const int token = t * p.tq + i_tok;            // of the unit
+        const int at0 = w.pos0 + t * p.tq, at = at0 + i_tok;   // positions: the row tile's first token, this row's
         const bool window = p.plan.window > 0;
-        const RowKeys keys{w.u.q.L, p.plan.causal ? token + diag : 0x7fffffff,
-                           window ? token + diag - p.plan.window + 1 : -0x7fffffff, p.plan.causal ? tok0 + diag : 0x7fffffff,
-                           window ? tok0 + p.tq - 1 + diag - p.plan.window + 1 : -0x7fffffff};
+        const RowKeys keys{w.L, p.plan.causal ? at : 0x7fffffff, window ? at - p.plan.window + 1 : -0x7fffffff,
+                           p.plan.causal ? at0 : 0x7fffffff, window ? at0 + p.tq - p.plan.window : -0x7fffffff};
         float m_ref = -INFINITY, l = 0.f;
         if (!softmax_tiles<C>(sbase, tmem, ctl, t, quarter, p.scale_log2, keys, js, je, scnt, ocnt, m_ref, l)) goto unwind;
         if (nk > 0) {
@@ -199,12 +270,13 @@ __device__ void paged_softmax_role(const PagedTileParams &p, PagedUnits<C> units
         {
             const float inv_l = l > 0.f ? 1.f / l : 0.f;
             const float lse = l > 0.f ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
-            const bool store = i_tok < p.tq && token < w.u.q.n;
-            const long long row = w.u.q.q0 + token;
-            const int head = w.u.g * p.pack + i_head;
+            const bool store = i_tok < p.tq && token < w.tokens;
+            const bool whole = w.slot < 0;
+            const long long row = w.row0 + token;
+            const int head = w.g * p.pack + i_head;
             const long long o_off = store ? (row * p.Hq + head) * D : -1;
             const long long piece = ((long long)w.slot * C::NQT + t) * kBlockQ + row_in_tile;
-            if (w.whole && C::OSTAGE) {
+            if (whole && C::OSTAGE) {
                 // 64 columns a pass through this warp's staging buffer (rows of 128 bytes, 16-byte unit i
                 // of row r at i ^ (r % 8)), so that eight lanes write one row's 128 bytes together.
                 const uint32_t stage = sbase + uint32_t(C::SMEM_OST + warp * C::OST_BYTES);
@@ -250,7 +322,7 @@ __device__ void paged_softmax_role(const PagedTileParams &p, PagedUnits<C> units
                         for (int i = 0; i < 32; ++i) o[i] = 0u;
                     }
                     if (!store) continue;
-                    if (!w.whole) {
+                    if (!whole) {
                         float *dst = p.o_part + piece * D + 32 * c;
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
@@ -274,7 +346,7 @@ __device__ void paged_softmax_role(const PagedTileParams &p, PagedUnits<C> units
             sm100::tc_fence_before_sync();
             sm100::mbar_arrive(bar(C::B_OEMPTY + t));
             if (store) {
-                if (!w.whole) p.lse_part[piece] = lse;
+                if (!whole) p.lse_part[piece] = lse;
                 else if (p.lse != nullptr) p.lse[(long long)head * p.plan.T + row] = lse;
             }
         }
@@ -298,6 +370,10 @@ fa_paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 
     if (threadIdx.x == 0) {
         init_barriers<C>(sbase);
+        for (int i = 0; i < kQueue; ++i) {
+            sm100::mbar_init(sbase + PlanSmem<C>::BARS + 8u * i, 1);
+            sm100::mbar_init(sbase + PlanSmem<C>::BARS + 8u * (kQueue + i), PlanSmem<C>::READERS);
+        }
         *abort_flag = 0;
         sm100::fence_mbar_init();
     }
@@ -305,24 +381,41 @@ fa_paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         sm100::tmem_alloc(sm100::smem_u32(tmem_holder), C::TMEM_COLS);
         sm100::tmem_relinquish();
     }
-    // The plan's sums use the K/V ring's memory before the first copy goes there.
-    static_assert(sizeof(PlanScan<C::THREADS>) + sizeof(Cursor) <= size_t(C::KV_TILE), "plan in the ring");
-    auto &scan = *reinterpret_cast<PlanScan<C::THREADS> *>(smem + C::SMEM_KV);
-    auto &start = *reinterpret_cast<Cursor *>(smem + C::SMEM_KV + sizeof(PlanScan<C::THREADS>));
-    const long long total = plan_scan<C::BC>(p.plan, scan, int(threadIdx.x), blockIdx.x == 0);
-    if (threadIdx.x == 0) {
-        const long long x0 = range_start(total, p.plan.workers, int(blockIdx.x));
-        const long long x1 = range_start(total, p.plan.workers, int(blockIdx.x) + 1);
+    // The plan uses the K/V ring's memory before the first copy goes there, but for the coarse counts.
+    struct Plan {
+        PlanScan<C::THREADS> scan;
+        long long cuts[kMaxPagedCtas + 1];
+        Cursor start;
+    };
+    static_assert(sizeof(Plan) <= size_t(C::NS) * C::KV_TILE, "plan in the ring");
+    static_assert(C::THREADS % kCoarse == 0 && C::THREADS >= kMaxPagedCtas, "segments, and a thread for each CTA");
+    Plan &plan = *reinterpret_cast<Plan *>(smem + C::SMEM_KV);
+    int *units_before = reinterpret_cast<int *>(smem + PlanSmem<C>::COARSE);
+    const int tid = int(threadIdx.x), seg = (p.plan.R + C::THREADS - 1) / C::THREADS, cta = int(blockIdx.x);
+    const long long total = plan_scan<C::BC>(p.plan, plan.scan, tid, cta == 0 && p.say != 0);
+    const int rounds = plan_schedule<C::BC>(p.plan, plan.scan, total, plan.cuts, tid);
+    if (tid <= kCoarse) units_before[tid] = plan.scan.seg_units[tid * (C::THREADS / kCoarse)];
+    if (cta == 0 && tid <= p.plan.workers) p.cuts[tid] = plan.cuts[tid];
+    if (tid == 0) {   // where this CTA's range begins, and what the merge has to do at that cut
+        const long long x0 = plan.cuts[cta], x1 = plan.cuts[cta + 1];
         Cursor c{};
-        if (x0 < x1) {
-            c.u = plan_find<C::BC>(p.plan, scan, x0);
+        MergeJob job{};
+        if (x0 < total) {
+            c.u = plan_find<C::BC>(p.plan, plan.scan, x0);
             c.j = c.u.js + int(x0 - c.u.begin);
             c.left = int(x1 - x0);
+            if (cta > 0) {
+                const long long end = c.u.begin + (c.u.je - c.u.js);
+                int last = cta - 1;
+                while (last + 1 < p.plan.workers && plan.cuts[last + 1] < end) ++last;
+                job = merge_job(p.plan, c.u, cta, plan.cuts[cta - 1], x0, last);
+            }
         }
-        start = c;
+        p.jobs[cta] = job;
+        plan.start = c;
     }
     __syncthreads();
-    const PagedUnits<C> units{p, start, true};
+    const Cursor start = plan.start;
     sm100::fence_proxy_async_smem();   // those reads and writes come before the copies into the ring
     sm100::tc_fence_before_sync();
     __syncthreads();
@@ -331,11 +424,14 @@ fa_paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 
     if (warp < C::SOFTMAX_WARPS) {
         if constexpr (C::REALLOC_REGS) sm100::regs_increase<C::SOFTMAX_REGS>();
-        paged_softmax_role<C>(p, units, sbase, tmem, ctl, warp, lane);
+        paged_softmax_role<C>(p, PagedUnits<C, kRoleSoftmax>{sbase, smem, ctl, p.box_rows, 0}, sbase, tmem, ctl, warp, lane);
     } else {
         if constexpr (C::REALLOC_REGS) sm100::regs_decrease<C::CONTROL_REGS>();
+        const PagedUnits<C, kRoleControl> units{sbase, smem, ctl, p.box_rows, 0};
         if (warp == C::TMA_WARP) paged_producer_role<C>(&tm_q, &tm_k, &tm_v, p, units, sbase, ctl);
         else if (warp == C::MMA_WARP) mma_role<C>(units, sbase, tmem, ctl);
+        else if (warp == C::MMA_WARP + 1 && lane == 0)
+            paged_plan_role<C>(p, units_before, seg * (C::THREADS / kCoarse), rounds * p.plan.workers, start, sbase, smem, ctl);
     }
     __syncwarp();
 
@@ -343,6 +439,24 @@ fa_paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     __syncthreads();
     sm100::tc_fence_after_sync();
     if (warp == 0) sm100::tmem_dealloc(tmem, C::TMEM_COLS);
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // ends after the kernel of few rows that it may run beside
+}
+
+// The merge after the tile kernel: blocks of 32 rows a cut, then (where the call has a kernel of few
+// rows too) that one's cuts.
+template <class C>
+__global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_constant__ PagedTileParams p,
+                                                             const __grid_constant__ PagedParams few) {
+    constexpr int kRows = C::NQT * kBlockQ, kPer = kRows / 32;
+    const int tile_blocks = (p.plan.workers - 1) * kPer, i = int(blockIdx.x);
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the pieces, cuts and jobs are written
+    if (i < tile_blocks) {
+        const int w = i / kPer + 1, row0 = i % kPer * 32;
+        merge_unit<C::D, C::F16, kRows, kBlockQ>(p, w, row0, row0 + 32,
+                                                 [&](int s) { return p.cuts[w - 1 + s] < p.cuts[w + s]; });
+    } else {
+        merge_unit<C::D, C::F16, kRowRows, kRowRows>(few, i - tile_blocks + 1, 0, kRowRows, [](int) { return true; });
+    }
 }
 
 }  // namespace fa

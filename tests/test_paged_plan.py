@@ -13,6 +13,7 @@ NVCC = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
 
 PROGRAM = r'''
 #include "fa_paged_plan.cuh"
+#include <algorithm>
 #include <cstdio>
 #include <random>
 #include <vector>
@@ -35,6 +36,8 @@ template <int KS, int NT> int check(std::mt19937 &rng, int round) {
     p.R = R;
     p.T = cu.back();
     p.max_new = 700;
+    p.n_lo = 1;
+    p.n_hi = 700;
     p.max_len = 1 << 20;
     p.causal = pick(0, 3) > 0;
     p.window = p.causal && pick(0, 1) ? pick(1, 900) : 0;
@@ -79,10 +82,16 @@ template <int KS, int NT> int check(std::mt19937 &rng, int round) {
     long long at = 0;
     for (int t = 0; t < NT; ++t) {
         sh.seg_start[t] = at;
+        sh.seg_units[t] = int(std::lower_bound(begin.begin(), begin.end(), at) - begin.begin());
         for (int r = t * seg; r < std::min(R, (t + 1) * seg); ++r) at += per_request[r];
     }
     sh.seg_start[NT] = at;
     if (at != total) return 6;
+    for (size_t i = 0; i < units.size(); ++i) {
+        const Unit u = plan_unit<KS>(p, sh.seg_units, NT, seg, int(i));
+        const Piece &e = units[i];
+        if (u.r != e.r || u.g != e.g || u.b != e.b || u.js != e.js || u.je != e.je) return 11;
+    }
     // the workers' walks
     size_t k = 0;
     long long x = 0;
