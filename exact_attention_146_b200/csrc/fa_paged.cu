@@ -106,6 +106,11 @@ template <bool H> using Tile128 = TileCfg<128, 128, 2, 4, 1, 1, true, 0, H, fals
 template <bool H> using Tile192 = TileCfg<192, 64, 2, 4, 1, 1, true, 0, H, false, false, true>;
 template <bool H> using Tile256 = TileCfg<256, 64, 1, 4, 1, 2, false, 0, H>;
 
+// What a unit of the tile kernel costs besides its key tiles (Q, the first tile's way through the
+// pipeline with nothing beside it, the epilogue), in key tiles: 7.5 us against 1.9 to 2.2 us a tile
+// (d = 128, 8 requests of up to 512 new tokens, 352 units).
+constexpr int kTileOverhead = 3;
+
 // The largest power of two, up to a key tile, that divides a page.
 int box_rows(int page, int most) {
     int g = 1;
@@ -127,7 +132,7 @@ int launch_tiles(const PagedParams &base, const View &q, View kv, const void *v,
                  cudaStream_t st) {
     static int state[kMaxDevices] = {};
     // the register split inside the kernel counts on exactly this launch budget
-    int rc = make_ready(fa_paged_tiles_kernel<C>, C::SMEM_BYTES, C::REALLOC_REGS ? C::LAUNCH_REGS : 0, state[dev]);
+    int rc = make_ready(fa_paged_tiles_kernel<C>, PlanSmem<C>::BYTES, C::REALLOC_REGS ? C::LAUNCH_REGS : 0, state[dev]);
     if (rc != FA_OK) return rc;
     PagedTileParams p{};
     static_cast<PagedParams &>(p) = base;
@@ -135,6 +140,7 @@ int launch_tiles(const PagedParams &base, const View &q, View kv, const void *v,
     p.plan.groups = p.Hq / p.pack;
     p.plan.tpb = C::NQT * p.tq;
     p.plan.workers = ctas;
+    p.plan.overhead = kTileOverhead;
     p.plan.n_lo = few + 1;
     p.box_rows = box_rows(p.page, C::BC);
     p.slot_first = p.slot_stride < p.head_stride ? 1 : 0;
@@ -155,10 +161,10 @@ int launch_tiles(const PagedParams &base, const View &q, View kv, const void *v,
     pf.say = 0;
     if (few > 0 && (rc = launch_rows<RowCfg<C::D, C::F16>>(pf, workspace, ctas, dev, st)) != FA_OK) return rc;
     if (few > 0) {   // beside the kernel before it, which began when the inputs were complete
-        rc = launch_after(fa_paged_tiles_kernel<C>, unsigned(ctas), C::THREADS, C::SMEM_BYTES, st, mq, mk, mv, p);
+        rc = launch_after(fa_paged_tiles_kernel<C>, unsigned(ctas), C::THREADS, PlanSmem<C>::BYTES, st, mq, mk, mv, p);
         if (rc != FA_OK) return rc;
     } else {
-        fa_paged_tiles_kernel<C><<<unsigned(ctas), C::THREADS, C::SMEM_BYTES, st>>>(mq, mk, mv, p);
+        fa_paged_tiles_kernel<C><<<unsigned(ctas), C::THREADS, PlanSmem<C>::BYTES, st>>>(mq, mk, mv, p);
         if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
     }
     const int blocks = (ctas - 1) * (rows / 32) + (few > 0 ? pf.plan.workers - 1 : 0);
@@ -282,7 +288,7 @@ size_t fa_paged_workspace_bytes(int Hq, int Hkv, int d) {
     if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || fa_tile_config(d, nullptr, nullptr, nullptr, nullptr) != FA_OK) return 0;
     return part_bytes(kMaxRowWorkers, kRowRows, d) + job_bytes(kMaxRowWorkers) +
            part_bytes(kMaxPagedCtas, d == 256 ? kBlockQ : 2 * kBlockQ, d) + job_bytes(kMaxPagedCtas) +
-           align256((kMaxPagedCtas + 1) * sizeof(long long));
+           align256(size_t(kMaxPagedCtas) * (kMaxPagedCtas + 1) * sizeof(long long));
 }
 
 int fa_paged_fwd(const void *q, long long q_stride, const fa_paged_cache *cache, const int *block_table,

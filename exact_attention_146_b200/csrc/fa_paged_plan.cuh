@@ -5,14 +5,15 @@
 //     last  = max(0, the block's last token + L - n)   (causal; L - 1 without a mask)
 //     first = max(0, the block's first token + L - n - W + 1)   (window W; else 0)
 //     js = first / KS,   je = last / KS + 1            (at least one tile, masked if need be).
-// Units in the order (r, g, b) are laid end to end on a line of key-tile steps, and the line is
+// Units in the order (r, g, b) are laid end to end on a line of steps, one a key tile and `overhead`
+// before them for what a unit costs besides, and the line is
 // cut into one equal range per worker (a CTA or a warp): every worker does the same number of
 // steps, whatever the mix of lengths, and a unit that a cut crosses is merged afterwards.
 //
 // The lengths are on the device, so every worker finds its own range.  The steps of a request are
 // a closed form: with A(c) = sum over blocks of floor(max(0, tpb b + c) / KS) (a floor sum, by the
-// Euclidean recursion), a group of nb blocks takes nb + A(tpb - 1 + L - n) - A(L - n - W + 1)
-// steps.  A block sums the requests once (each thread a contiguous segment of them), scans the
+// Euclidean recursion), a group of nb blocks takes nb (1 + overhead) + A(tpb - 1 + L - n) -
+// A(L - n - W + 1) steps.  A block sums the requests once (each thread a contiguous segment of them), scans the
 // segment sums, and a worker finds its place by bisection.
 #pragma once
 
@@ -34,6 +35,7 @@ struct PlanParams {
     int groups;                    // head groups a request: Hq / pack
     int tpb;                       // new tokens a unit
     int workers;
+    int overhead;                  // steps that a unit costs besides its key tiles
 };
 
 struct Request {
@@ -119,7 +121,7 @@ FA_PLAN long long plan_steps(const PlanParams &p, const Request &q, int nb) {
     if (nb <= 0) return 0;
     int js, je;
     plan_range<KS>(p, q, nb - 1, js, je);   // the last block apart: it may be short
-    long long s = je - js;
+    long long s = je - js + (long long)nb * p.overhead;
     if (nb > 1) {
         const long long diag = (long long)q.L - q.n;
         s += nb - 1;
@@ -213,18 +215,60 @@ struct Unit {
     long long begin;   // first step on the line
 };
 
-// The unit that step x (0 <= x < total) lies in.
-template <int KS, int NT>
-FA_PLAN Unit plan_find(const PlanParams &p, const PlanScan<NT> &sh, long long x) {
-    int lo = 0, hi = NT;
+FA_PLAN int plan_length(const PlanParams &p, const Unit &u) { return u.je - u.js + p.overhead; }
+
+// The block of a request's head group that step x of the group lies in, and the steps before it.
+// On the device a whole warp looks through 32 blocks at a time.
+template <int KS>
+FA_PLAN int find_block(const PlanParams &p, const Request &q, long long x, long long &before) {
+    const int nb = plan_blocks(p, q);
+    before = 0;
+#ifdef __CUDA_ARCH__
+    const int lane = int(threadIdx.x) % 32;
+    for (int b0 = 0; b0 < nb; b0 += 32) {
+        int len = 0;
+        if (b0 + lane < nb) {
+            int js, je;
+            plan_range<KS>(p, q, b0 + lane, js, je);
+            len = je - js + p.overhead;
+        }
+        long long upto = len;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, b0 + lane < nb && before + upto > x);
+        if (past != 0) {
+            const int at = __ffs(int(past)) - 1;
+            before += __shfl_sync(0xffffffffu, upto - len, at);
+            return b0 + at;
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return nb - 1;
+#else
+    for (int b = 0;; ++b) {
+        int js, je;
+        plan_range<KS>(p, q, b, js, je);
+        if (b == nb - 1 || before + je - js + p.overhead > x) return b;
+        before += je - js + p.overhead;
+    }
+#endif
+}
+
+// The unit that step x (0 <= x < total) lies in; by all threads of a warp.  `steps_before` are the
+// steps before each of `segments` segments of `seg` requests.
+template <int KS>
+FA_PLAN Unit plan_find(const PlanParams &p, const long long *steps_before, int segments, int seg, long long x) {
+    int lo = 0, hi = segments;
     while (hi - lo > 1) {   // the last segment that begins at or before x
         const int mid = (lo + hi) / 2;
-        if (sh.seg_start[mid] <= x) lo = mid;
+        if (steps_before[mid] <= x) lo = mid;
         else hi = mid;
     }
-    const int seg = (p.R + NT - 1) / NT;
     Unit u{};
-    long long at = sh.seg_start[lo], group = 0;
+    long long at = steps_before[lo], group = 0;
     for (u.r = lo * seg; u.r < p.R; ++u.r) {
         u.q = load_request(p, u.r);
         if (u.q.n == 0) continue;
@@ -234,14 +278,9 @@ FA_PLAN Unit plan_find(const PlanParams &p, const PlanScan<NT> &sh, long long x)
     }
     u.g = int(div_pos(x - at, group));
     at += u.g * group;
-    int b_lo = 0, b_hi = plan_blocks(p, u.q);
-    while (b_hi - b_lo > 1) {
-        const int mid = (b_lo + b_hi) / 2;
-        if (at + plan_steps<KS>(p, u.q, mid) <= x) b_lo = mid;
-        else b_hi = mid;
-    }
-    u.b = b_lo;
-    u.begin = at + plan_steps<KS>(p, u.q, b_lo);
+    long long before;
+    u.b = find_block<KS>(p, u.q, x - at, before);
+    u.begin = at + before;
     plan_range<KS>(p, u.q, u.b, u.js, u.je);
     return u;
 }
@@ -274,7 +313,7 @@ FA_PLAN Unit plan_unit(const PlanParams &p, const int *units_before, int segment
 // The next unit of the line (there is one).
 template <int KS>
 FA_PLAN void plan_next(const PlanParams &p, Unit &u) {
-    u.begin += u.je - u.js;
+    u.begin += plan_length(p, u);
     if (++u.b >= plan_blocks(p, u.q)) {
         u.b = 0;
         if (++u.g >= p.groups) {
@@ -288,6 +327,12 @@ FA_PLAN void plan_next(const PlanParams &p, Unit &u) {
     plan_range<KS>(p, u.q, u.b, u.js, u.je);
 }
 
+// CTAs that a call is worth: each with at least kLeastShare steps (its overhead among them).
+constexpr int kLeastShare = 6;
+FA_PLAN int plan_active(const PlanParams &p, long long total) {
+    return int(max(1LL, min((long long)p.workers, total / kLeastShare)));
+}
+
 // The schedule of the CTAs of a tile kernel, in two phases.  First whole units, CTA c units c,
 // c + G, c + 2 G, ...: CTAs that run at the same time have neighbouring units, the token blocks of one
 // head, and go through its keys side by side, so that K and V come from L2.  As many rounds of G units
@@ -296,8 +341,8 @@ FA_PLAN void plan_next(const PlanParams &p, Unit &u) {
 // By all NT >= G threads; `cuts` is shared memory for G + 1 places.  Returns the rounds.
 template <int KS, int NT>
 __device__ inline int plan_schedule(const PlanParams &p, PlanScan<NT> &sh, long long total, long long *cuts, int tid) {
-    const int G = p.workers, units = sh.seg_units[NT], seg = (p.R + NT - 1) / NT;
-    const long long share = tid < G ? range_start(total, G, tid + 1) - range_start(total, G, tid) : 0;
+    const int G = p.workers, active = plan_active(p, total), units = sh.seg_units[NT], seg = (p.R + NT - 1) / NT;
+    const long long share = tid < active ? range_start(total, active, tid + 1) - range_start(total, active, tid) : 0;
     long long mine = 0;
     int rounds = 0;
     for (;; ++rounds) {
@@ -308,7 +353,7 @@ __device__ inline int plan_schedule(const PlanParams &p, PlanScan<NT> &sh, long 
             stop = k >= units;
             if (!stop) {
                 const Unit u = plan_unit<KS>(p, sh.seg_units, NT, seg, int(k));
-                len = u.je - u.js;
+                len = plan_length(p, u);
                 stop = mine + len > share;
             }
         }
@@ -323,13 +368,48 @@ __device__ inline int plan_schedule(const PlanParams &p, PlanScan<NT> &sh, long 
     return rounds;
 }
 
-// The merge job of cut w, which lies at `cut` in unit u, where the worker before begins at `before` and
-// the unit's last step is done by worker `last`.
-FA_PLAN MergeJob merge_job(const PlanParams &p, const Unit &u, int w, long long before, long long cut, int last) {
+// A range of the line, from step o of unit u on.  The steps of a unit's overhead have no tiles: a
+// cut among them leaves the unit whole to the worker behind it.
+struct Walk {
+    Unit u;
+    long long o, left;
+    bool first;        // the next piece is the range's first
+};
+struct Piece {
+    Unit u;
+    int js, je;        // key tiles
+    bool first;
+};
+
+// The next piece that has tiles; false at the end of the range.
+template <int KS>
+FA_PLAN bool walk_next(const PlanParams &p, Walk &w, Piece &piece) {
+    while (w.left > 0) {
+        const long long len = plan_length(p, w.u), end = min(len, w.o + w.left);
+        piece.u = w.u;
+        piece.js = w.u.js + int(max(0LL, w.o - p.overhead));
+        piece.je = w.u.js + int(max(0LL, end - p.overhead));
+        piece.first = w.first;
+        w.first = false;
+        w.left -= end - w.o;
+        w.o = 0;
+        if (w.left > 0) plan_next<KS>(p, w.u);
+        if (piece.je > piece.js) return true;
+    }
+    return false;
+}
+
+// The merge job of cut w (w >= 1), which lies at cuts[w] in unit u; cuts[0 .. workers].
+template <class Cuts>
+FA_PLAN MergeJob merge_job(const PlanParams &p, const Unit &u, int w, int workers, const Cuts &cuts) {
     MergeJob j{};
-    if (before == cut || u.begin >= cut || before > u.begin) return j;
+    const long long cut = cuts(w), before = cuts(w - 1), end = u.begin + plan_length(p, u);
+    // tiles on both sides, and none of the unit's cuts before this one has
+    if (before == cut || cut - u.begin <= p.overhead || before - u.begin > p.overhead) return j;
+    int last = w;
+    while (last + 1 < workers && cuts(last + 1) < end) ++last;
     j.parts = last - (w - 1) + 1;
-    j.first_slot = 2 * (w - 1) + (before == u.begin ? 0 : 1);
+    j.first_slot = 2 * (w - 1) + (before >= u.begin ? 0 : 1);
     j.row0 = u.q.q0 + u.b * p.tpb;
     j.tokens = min(u.q.n - u.b * p.tpb, p.tpb);
     j.g = u.g;

@@ -133,24 +133,28 @@ __global__ void __launch_bounds__(C::THREADS, 1) fa_paged_rows_kernel(const __gr
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge may be set up meanwhile
     const int lane = int(threadIdx.x) % 32, warp = int(threadIdx.x) / 32;
     const long long total = plan_scan<kRowKeys>(p.plan, scan, int(threadIdx.x), blockIdx.x == 0 && p.say != 0);
-    const int worker = int(blockIdx.x) * C::WARPS + warp;
-    const long long x0 = range_start(total, p.plan.workers, worker);
-    const long long x1 = range_start(total, p.plan.workers, worker + 1);
+    // Neighbouring workers are on different SMs, so that few of them spread out.
+    const int worker = warp * int(gridDim.x) + int(blockIdx.x);
+    // A call too small for all: a unit of U steps in pieces of s costs s steps and then the merge of U / s
+    // pieces, eight loads of them at a time; with a step and such a round about equally long, s^2 = U / 8.
+    const float mean = float(total) / float(max(1, scan.seg_units[C::THREADS]));
+    const long long least = max(2LL, (long long)sqrtf(mean * 0.125f));
+    const int workers = int(max(1LL, min((long long)p.plan.workers, total / least)));
+    const long long x0 = worker < workers ? range_start(total, workers, worker) : total;
+    const long long x1 = worker < workers ? range_start(total, workers, worker + 1) : total;
     if (x0 >= x1) {
         if (lane == 0) p.jobs[worker].parts = 0;
         return;
     }
 
     Cursor load;
-    load.u = plan_find<kRowKeys>(p.plan, scan, x0);
+    load.u = plan_find<kRowKeys>(p.plan, scan.seg_start, C::THREADS, (p.plan.R + C::THREADS - 1) / C::THREADS, x0);
     load.j = load.u.js + int(x0 - load.u.begin);
     load.left = int(min(x1 - x0, 0x7fffffffLL));
     Cursor cur = load;
     if (lane == 0) {
         MergeJob job{};
-        if (worker > 0 && load.u.begin < x0)
-            job = merge_job(p.plan, load.u, worker, range_start(total, p.plan.workers, worker - 1), x0,
-                            range_owner(total, p.plan.workers, load.u.begin + (load.u.je - load.u.js) - 1));
+        if (worker > 0) job = merge_job(p.plan, load.u, worker, workers, [&](int w) { return range_start(total, workers, w); });
         p.jobs[worker] = job;
     }
 

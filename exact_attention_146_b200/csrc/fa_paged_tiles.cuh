@@ -24,10 +24,10 @@ struct PagedTileParams : PagedParams {
     int tq;            // tokens a row tile: 128 / pack
     int box_rows;      // slots a K/V box
     int slot_first;    // the tensor map's second axis is the slot (else the head)
-    long long *cuts;   // workspace: [workers + 1] the cuts of the line, for the merge
+    long long *cuts;   // workspace: the cuts of the line, each CTA's copy (kMaxPagedCtas + 1 places)
 };
 
-// The units before each of 64 segments of the requests: what the planner needs to find whole units.
+// The units and steps before each of 64 segments of the requests: what the planner finds its units by.
 constexpr int kCoarse = 64;
 constexpr int kQueue = 4;   // units planned ahead
 
@@ -43,14 +43,18 @@ struct PagedUnit {
     int pad;
 };
 
-// Shared memory between the pipeline's barriers and the staging: the queue's barriers (full, empty),
-// its entries, and the coarse counts.
+// Shared memory of the plan, between the pipeline's barriers and the staging and behind it: the
+// queue's barriers (full, empty), its entries, and the coarse counts.
 template <class C>
 struct PlanSmem {
     static constexpr int BARS = C::SMEM_MISC + 16;
     static constexpr int UNITS = BARS + 2 * kQueue * 8;
     static constexpr int COARSE = UNITS + kQueue * int(sizeof(PagedUnit));
+    static constexpr int STEPS = C::SMEM_OST + 4 * C::NQT * C::OST_BYTES;   // behind the staging
+    static constexpr int RANGE = STEPS + (kCoarse + 1) * 8;                // this CTA's cut and the cuts beside it
+    static constexpr int BYTES = C::SMEM_BYTES + 1024;
     static_assert(COARSE + (kCoarse + 1) * 4 <= C::SMEM_OST, "the plan lies before the staging");
+    static_assert(RANGE + 64 + 1024 <= BYTES && BYTES <= 232448, "shared memory budget");
     static_assert(BARS % 8 == 0 && sizeof(PagedUnit) == 64, "alignment");
     // who hands an entry back: the TMA warp, the MMA warp and each softmax warp
     static constexpr int READERS = 2 + C::SOFTMAX_WARPS;
@@ -93,43 +97,50 @@ struct PagedUnits {
     }
 };
 
-// The planner: one thread walks this CTA's units (its whole ones, then its range of the line) and
-// queues them, so that the other roles do none of the plan's arithmetic.
+// The planner: one warp walks this CTA's units (its whole ones, then its range of the line) and queues
+// them, so that the other roles do none of the plan's arithmetic.
 template <class C>
-__device__ void paged_plan_role(const PagedTileParams &p, const int *units_before, int seg, int whole_units, Cursor at,
-                                uint32_t sbase, uint8_t *smem, const Ctl &ctl) {
-    bool first = true;
-    int k = int(blockIdx.x);
+__device__ void paged_plan_role(const PagedTileParams &p, int seg, int whole_units, uint32_t sbase, uint8_t *smem, const Ctl &ctl) {
+    const int lane = int(threadIdx.x) % 32, cta = int(blockIdx.x);
+    const int *units_before = reinterpret_cast<const int *>(smem + PlanSmem<C>::COARSE);
+    const long long *steps_before = reinterpret_cast<const long long *>(smem + PlanSmem<C>::STEPS);
+    const long long *range = reinterpret_cast<const long long *>(smem + PlanSmem<C>::RANGE);
+    const long long x0 = range[0], x1 = range[1], total = range[2];
     const uint32_t bars = sbase + PlanSmem<C>::BARS;
+    Walk walk{};
+    bool found = false;
+    int k = cta;
 #pragma unroll 1
     for (uint32_t n = 0;; ++n) {
         PagedUnit w{};
         w.tokens = -1;
-        Unit u{};
-        int pjs = 0, pje = 0;
+        Piece piece{};
         if (k < whole_units) {
-            u = plan_unit<C::BC>(p.plan, units_before, kCoarse, seg, k);
-            pjs = u.js;
-            pje = u.je;
+            piece.u = plan_unit<C::BC>(p.plan, units_before, kCoarse, seg, k);
+            piece.js = piece.u.js;
+            piece.je = piece.u.je;
             k += p.plan.workers;
-            w.slot = -1;
             w.tokens = 0;
-        } else if (at.left > 0) {
-            u = at.u;
-            pjs = at.j;
-            pje = min(u.je, at.j + at.left);
-            w.slot = pjs == u.js && pje == u.je ? -1 : 2 * int(blockIdx.x) + (first ? 0 : 1);
-            w.tokens = 0;
-            first = false;
-            at.left -= pje - pjs;
-            if (at.left > 0) {
-                plan_next<C::BC>(p.plan, at.u);
-                at.j = at.u.js;
+        } else {
+            if (!found) {   // where the range begins, and what the merge has to do at that cut
+                found = true;
+                MergeJob job{};
+                if (x0 < total) {
+                    walk.u = plan_find<C::BC>(p.plan, steps_before, kCoarse, seg, x0);
+                    walk.o = x0 - walk.u.begin;
+                    walk.left = x1 - x0;
+                    walk.first = true;
+                    if (cta > 0) job = merge_job(p.plan, walk.u, cta, p.plan.workers, [&](int c) { return p.cuts[cta * (kMaxPagedCtas + 1) + c]; });
+                }
+                if (lane == 0) p.jobs[cta] = job;
             }
+            if (walk_next<C::BC>(p.plan, walk, piece)) w.tokens = 0;
         }
         if (w.tokens == 0) {
+            const Unit &u = piece.u;
             const long long diag = (long long)u.q.L - u.q.n;
             const int tok0 = u.b * p.plan.tpb;
+            w.slot = piece.js == u.js && piece.je == u.je ? -1 : 2 * cta + (piece.first ? 0 : 1);
             w.row0 = u.q.q0 + tok0;
             w.tokens = min(u.q.n - tok0, p.plan.tpb);
             w.pos0 = int(tok0 + diag);
@@ -144,7 +155,7 @@ __device__ void paged_plan_role(const PagedTileParams &p, const int *units_befor
                 if (t0 >= t1) continue;
                 const int last = p.plan.causal ? w.pos0 + t1 - 1 : w.L - 1;
                 const int from = p.plan.window > 0 ? w.pos0 + t0 - p.plan.window + 1 : 0;
-                const int js = max(max(from, 0) / C::BC, pjs), je = min(max(last, 0) / C::BC + 1, pje);
+                const int js = max(max(from, 0) / C::BC, piece.js), je = min(max(last, 0) / C::BC + 1, piece.je);
                 if (je <= js) continue;
                 w.js[t] = js;
                 w.je[t] = je;
@@ -154,9 +165,11 @@ __device__ void paged_plan_role(const PagedTileParams &p, const int *units_befor
             if (w.j_hi == 0) w.j_lo = 0;
         }
         const int i = int(n % kQueue);
-        if (!wait_bar<kRoleControl>(bars + 8u * (kQueue + i), ((n / kQueue) & 1u) ^ 1u, ctl, kSiteUnitEmpty)) return;
-        *reinterpret_cast<PagedUnit *>(smem + PlanSmem<C>::UNITS + i * int(sizeof(PagedUnit))) = w;
-        sm100::mbar_arrive(bars + 8u * i);
+        if (!warp_wait_bar<kRoleControl>(bars + 8u * (kQueue + i), ((n / kQueue) & 1u) ^ 1u, ctl, kSiteUnitEmpty)) return;
+        if (lane == 0) {
+            *reinterpret_cast<PagedUnit *>(smem + PlanSmem<C>::UNITS + i * int(sizeof(PagedUnit))) = w;
+            sm100::mbar_arrive(bars + 8u * i);
+        }
         if (w.tokens < 0) return;
     }
 }
@@ -311,7 +324,39 @@ __device__ void paged_softmax_role(const PagedTileParams &p, PagedUnits<C, kRole
                     }
                     __syncwarp();
                 }
+            } else if (!whole && C::OSTAGE) {
+                // the piece's fp32 rows, 32 columns a pass through the same buffer
+                const uint32_t stage = sbase + uint32_t(C::SMEM_OST + warp * C::OST_BYTES);
+                const unsigned stored = __ballot_sync(0xffffffffu, store);
+                float *dst = p.o_part + (piece - lane) * D;   // the warp's first row
+#pragma unroll 1
+                for (int c = 0; c < C::O_CHUNKS; ++c) {
+                    uint32_t o[32];
+                    if (nk > 0) {
+                        sm100::tmem_ld32_sync(o_taddr + uint32_t(32 * c), o);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = 0u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv_l);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        sm100::st_shared_v4(stage + uint32_t(lane * 128 + ((i ^ (lane & 7)) * 16)), o[4 * i], o[4 * i + 1], o[4 * i + 2],
+                                            o[4 * i + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int rr = 4 * i + lane / 8, col = 32 * c + 4 * (lane % 8);
+                        uint32_t x[4];
+                        sm100::ld_shared_v4(x, stage + uint32_t(rr * 128 + (((lane % 8) ^ (rr & 7)) * 16)));
+                        if ((stored >> rr & 1u) && col < D)
+                            *reinterpret_cast<uint4 *>(dst + rr * D + col) = make_uint4(x[0], x[1], x[2], x[3]);
+                    }
+                    __syncwarp();
+                }
             } else {
+                // d = 32: a row's 64 (whole) or 128 bytes by its own thread
 #pragma unroll
                 for (int c = 0; c < C::O_CHUNKS; ++c) {
                     uint32_t o[32];
@@ -326,14 +371,12 @@ __device__ void paged_softmax_role(const PagedTileParams &p, PagedUnits<C, kRole
                         float *dst = p.o_part + piece * D + 32 * c;
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            if (32 * c + 4 * i < D)
-                                *reinterpret_cast<float4 *>(dst + 4 * i) =
-                                    make_float4(__uint_as_float(o[4 * i]) * inv_l, __uint_as_float(o[4 * i + 1]) * inv_l,
-                                                __uint_as_float(o[4 * i + 2]) * inv_l, __uint_as_float(o[4 * i + 3]) * inv_l);
+                            *reinterpret_cast<float4 *>(dst + 4 * i) =
+                                make_float4(__uint_as_float(o[4 * i]) * inv_l, __uint_as_float(o[4 * i + 1]) * inv_l,
+                                            __uint_as_float(o[4 * i + 2]) * inv_l, __uint_as_float(o[4 * i + 3]) * inv_l);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            if (32 * c + 8 * i >= D) continue;
                             uint32_t x[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
@@ -385,37 +428,25 @@ fa_paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     struct Plan {
         PlanScan<C::THREADS> scan;
         long long cuts[kMaxPagedCtas + 1];
-        Cursor start;
     };
     static_assert(sizeof(Plan) <= size_t(C::NS) * C::KV_TILE, "plan in the ring");
-    static_assert(C::THREADS % kCoarse == 0 && C::THREADS >= kMaxPagedCtas, "segments, and a thread for each CTA");
+    static_assert(C::THREADS % kCoarse == 0 && C::THREADS > kMaxPagedCtas, "segments, and a thread for each cut");
     Plan &plan = *reinterpret_cast<Plan *>(smem + C::SMEM_KV);
-    int *units_before = reinterpret_cast<int *>(smem + PlanSmem<C>::COARSE);
     const int tid = int(threadIdx.x), seg = (p.plan.R + C::THREADS - 1) / C::THREADS, cta = int(blockIdx.x);
     const long long total = plan_scan<C::BC>(p.plan, plan.scan, tid, cta == 0 && p.say != 0);
     const int rounds = plan_schedule<C::BC>(p.plan, plan.scan, total, plan.cuts, tid);
-    if (tid <= kCoarse) units_before[tid] = plan.scan.seg_units[tid * (C::THREADS / kCoarse)];
-    if (cta == 0 && tid <= p.plan.workers) p.cuts[tid] = plan.cuts[tid];
-    if (tid == 0) {   // where this CTA's range begins, and what the merge has to do at that cut
-        const long long x0 = plan.cuts[cta], x1 = plan.cuts[cta + 1];
-        Cursor c{};
-        MergeJob job{};
-        if (x0 < total) {
-            c.u = plan_find<C::BC>(p.plan, plan.scan, x0);
-            c.j = c.u.js + int(x0 - c.u.begin);
-            c.left = int(x1 - x0);
-            if (cta > 0) {
-                const long long end = c.u.begin + (c.u.je - c.u.js);
-                int last = cta - 1;
-                while (last + 1 < p.plan.workers && plan.cuts[last + 1] < end) ++last;
-                job = merge_job(p.plan, c.u, cta, plan.cuts[cta - 1], x0, last);
-            }
-        }
-        p.jobs[cta] = job;
-        plan.start = c;
+    if (tid <= kCoarse) {
+        reinterpret_cast<int *>(smem + PlanSmem<C>::COARSE)[tid] = plan.scan.seg_units[tid * (C::THREADS / kCoarse)];
+        reinterpret_cast<long long *>(smem + PlanSmem<C>::STEPS)[tid] = plan.scan.seg_start[tid * (C::THREADS / kCoarse)];
     }
+    if (tid == 0) {
+        long long *range = reinterpret_cast<long long *>(smem + PlanSmem<C>::RANGE);
+        range[0] = plan.cuts[cta];
+        range[1] = plan.cuts[cta + 1];
+        range[2] = total;
+    }
+    if (tid <= p.plan.workers) p.cuts[cta * (kMaxPagedCtas + 1) + tid] = plan.cuts[tid];   // the planner and the merge read them
     __syncthreads();
-    const Cursor start = plan.start;
     sm100::fence_proxy_async_smem();   // those reads and writes come before the copies into the ring
     sm100::tc_fence_before_sync();
     __syncthreads();
@@ -430,8 +461,8 @@ fa_paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         const PagedUnits<C, kRoleControl> units{sbase, smem, ctl, p.box_rows, 0};
         if (warp == C::TMA_WARP) paged_producer_role<C>(&tm_q, &tm_k, &tm_v, p, units, sbase, ctl);
         else if (warp == C::MMA_WARP) mma_role<C>(units, sbase, tmem, ctl);
-        else if (warp == C::MMA_WARP + 1 && lane == 0)
-            paged_plan_role<C>(p, units_before, seg * (C::THREADS / kCoarse), rounds * p.plan.workers, start, sbase, smem, ctl);
+        else if (warp == C::MMA_WARP + 1)
+            paged_plan_role<C>(p, seg * (C::THREADS / kCoarse), rounds * p.plan.workers, sbase, smem, ctl);
     }
     __syncwarp();
 

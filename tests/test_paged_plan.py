@@ -14,12 +14,13 @@ NVCC = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
 PROGRAM = r'''
 #include "fa_paged_plan.cuh"
 #include <algorithm>
+#include <array>
 #include <cstdio>
 #include <random>
 #include <vector>
 using namespace fa;
 
-struct Piece { int r, g, b, js, je; };
+struct Listed { int r, g, b, js, je; };
 
 template <int KS, int NT> int check(std::mt19937 &rng, int round) {
     auto pick = [&](int lo, int hi) { return std::uniform_int_distribution<int>(lo, hi)(rng); };
@@ -44,8 +45,9 @@ template <int KS, int NT> int check(std::mt19937 &rng, int round) {
     p.groups = pick(1, 5);
     p.tpb = pick(0, 1) ? pick(1, 16) : (1 << pick(0, 8));
     p.workers = pick(1, 40);
+    p.overhead = pick(0, 4);
     // counting
-    std::vector<Piece> units;
+    std::vector<Listed> units;
     std::vector<long long> begin{0};
     PlanScan<NT> sh{};
     const int seg = (R + NT - 1) / NT;
@@ -70,11 +72,11 @@ template <int KS, int NT> int check(std::mt19937 &rng, int round) {
                 if (hi >= 0 && (lo / KS < js || hi / KS >= je)) return 2;      // a visible key left out
                 if (hi >= 0 && je != hi / KS + 1) return 3;                    // more tiles than needed
                 if (je <= js || js < 0) return 4;
-                group += je - js;
+                group += je - js + p.overhead;
                 if (plan_steps<KS>(p, q, b + 1) != group) return 5;
                 units.push_back({r, g, b, js, je});
-                begin.push_back(begin.back() + je - js);
-                per_request[r] += je - js;
+                begin.push_back(begin.back() + je - js + p.overhead);
+                per_request[r] += je - js + p.overhead;
             }
         }
     }
@@ -89,7 +91,7 @@ template <int KS, int NT> int check(std::mt19937 &rng, int round) {
     if (at != total) return 6;
     for (size_t i = 0; i < units.size(); ++i) {
         const Unit u = plan_unit<KS>(p, sh.seg_units, NT, seg, int(i));
-        const Piece &e = units[i];
+        const Listed &e = units[i];
         if (u.r != e.r || u.g != e.g || u.b != e.b || u.js != e.js || u.je != e.je) return 11;
     }
     // the workers' walks
@@ -100,16 +102,74 @@ template <int KS, int NT> int check(std::mt19937 &rng, int round) {
         if (x0 != x || x1 < x0 || x1 - x0 > total / p.workers + 1) return 7;
         if (x1 == x0) continue;
         if (range_owner(total, p.workers, x0) != w || range_owner(total, p.workers, x1 - 1) != w) return 8;
-        Unit u = plan_find<KS>(p, sh, x0);
+        Unit u = plan_find<KS>(p, sh.seg_start, NT, seg, x0);
         while (x < x1) {
             while (begin[k + 1] <= x) ++k;
-            const Piece &e = units[k];
+            const Listed &e = units[k];
             if (u.r != e.r || u.g != e.g || u.b != e.b || u.js != e.js || u.je != e.je || u.begin != begin[k]) return 9;
             x = std::min(x1, begin[k + 1]);
             if (x < x1) plan_next<KS>(p, u);
         }
     }
-    return x == total ? 0 : 10;
+    if (x != total) return 10;
+    // pieces and merge jobs, for even cuts and for uneven ones (empty ranges among them)
+    for (int kind = 0; kind < 2; ++kind) {
+        std::vector<long long> cuts;
+        const long long x0 = kind ? begin[pick(0, int(units.size()))] : 0;   // the rest of a line behind whole units
+        for (int w = 0; w <= p.workers; ++w)
+            cuts.push_back(kind ? x0 + (total - x0 > 0 ? std::uniform_int_distribution<long long>(0, total - x0)(rng) : 0)
+                                : range_start(total, p.workers, w));
+        std::sort(cuts.begin(), cuts.end());
+        cuts.front() = x0;
+        cuts.back() = total;
+        auto cut_at = [&](int w) { return cuts[w]; };
+        std::vector<std::vector<std::array<int, 3>>> done(units.size());   // pieces (js, je, slot) of each unit; slot -1: whole
+        for (int w = 0; w < p.workers; ++w) {
+            if (cuts[w] >= total) continue;
+            Walk walk{};
+            walk.u = plan_find<KS>(p, sh.seg_start, NT, seg, cuts[w]);
+            walk.o = cuts[w] - walk.u.begin;
+            walk.left = cuts[w + 1] - cuts[w];
+            walk.first = true;
+            Piece piece;
+            int slots = 0;
+            while (walk_next<KS>(p, walk, piece)) {
+                const size_t i = std::lower_bound(begin.begin(), begin.end(), piece.u.begin) - begin.begin();
+                const bool whole = piece.js == piece.u.js && piece.je == piece.u.je;
+                const int slot = whole ? -1 : 2 * w + (piece.first ? 0 : 1);
+                if (!whole && (slots & (piece.first ? 1 : 2))) return 12;   // a slot used twice
+                if (!whole) slots |= piece.first ? 1 : 2;
+                done[i].push_back({piece.js, piece.je, slot});
+            }
+        }
+        std::vector<int> merged(units.size(), 0);
+        for (int w = 1; w < p.workers; ++w) {
+            if (cuts[w] >= total) continue;
+            const Unit u = plan_find<KS>(p, sh.seg_start, NT, seg, cuts[w]);
+            const MergeJob job = merge_job(p, u, w, p.workers, cut_at);
+            if (job.parts == 0) continue;
+            const size_t i = std::lower_bound(begin.begin(), begin.end(), u.begin) - begin.begin();
+            if (merged[i]++) return 13;
+            std::vector<int> slots;
+            for (int s = 0; s < job.parts; ++s)
+                if (cuts[w - 1 + s] < cuts[w + s]) slots.push_back(s == 0 ? job.first_slot : 2 * (w - 1 + s));
+            if (slots.size() != done[i].size()) return 14;
+            for (size_t s = 0; s < slots.size(); ++s)
+                if (slots[s] != done[i][s][2]) return 15;
+            if (job.row0 != cu[u.r] + u.b * p.tpb || job.g != u.g) return 16;
+        }
+        for (size_t i = 0; i < units.size(); ++i) {
+            if (begin[i] < x0) continue;
+            int js = units[i].js;
+            for (auto &d : done[i]) {
+                if (d[0] != js || d[1] <= d[0]) return 17;
+                js = d[1];
+            }
+            if (js != units[i].je) return 18;
+            if ((done[i].size() > 1) != (merged[i] == 1)) return 19;
+        }
+    }
+    return 0;
 }
 
 int main() {
