@@ -88,8 +88,8 @@ int current_device(DeviceState **out, int *dev_out) {
 }
 
 // `bytes` starting at `p` must be device (or managed) memory of device `dev`, inside one
-// allocation.
-int check_device_range(const void *p, size_t bytes, int dev) {
+// allocation; [lo, hi) is set to that allocation (to the bytes themselves if it cannot be asked for).
+static int device_range(const void *p, size_t bytes, int dev, uintptr_t *lo, uintptr_t *hi) {
     cudaPointerAttributes a{};
     if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
         cudaGetLastError();
@@ -97,21 +97,41 @@ int check_device_range(const void *p, size_t bytes, int dev) {
     }
     if (!(a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged) || a.device != dev)
         return FA_ERR_NOT_DEVICE_MEMORY;
+    *lo = reinterpret_cast<uintptr_t>(p);
+    *hi = *lo + bytes;
     if (AddressRangeFn fn = address_range_fn()) {
         CUdeviceptr base = 0;
         size_t size = 0;
         if (fn(&base, &size, reinterpret_cast<CUdeviceptr>(p)) != CUDA_SUCCESS)
             return FA_ERR_NOT_DEVICE_MEMORY;
-        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-        if (lo + bytes > uintptr_t(base) + size) return FA_ERR_NOT_DEVICE_MEMORY;
+        if (*hi > uintptr_t(base) + size) return FA_ERR_NOT_DEVICE_MEMORY;
+        *lo = uintptr_t(base);
+        *hi = uintptr_t(base) + size;
     }
     return FA_OK;
 }
 
-int check_spans(const Span *s, int n, int dev) {
-    for (int i = 0; i < n; ++i)
-        if (s[i].bytes > 0)
-            if (const int rc = check_device_range(s[i].p, s[i].bytes, dev)) return rc;
+int check_device_range(const void *p, size_t bytes, int dev) {
+    uintptr_t lo, hi;
+    return device_range(p, bytes, dev, &lo, &hi);
+}
+
+// An array inside an allocation that this call has asked about already is not asked about again
+// (a caching allocator hands out small arrays from one): the two driver queries take about 0.7 us.
+int check_spans(SpanRanges *seen, const Span *s, int n, int dev) {
+    for (int i = 0; i < n; ++i) {
+        if (s[i].bytes == 0) continue;
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(s[i].p), hi = lo + s[i].bytes;
+        bool known = false;
+        for (int r = 0; r < seen->n && !known; ++r) known = lo >= seen->lo[r] && hi <= seen->hi[r];
+        if (known) continue;
+        uintptr_t a = 0, b = 0;
+        if (const int rc = device_range(s[i].p, s[i].bytes, dev, &a, &b)) return rc;
+        if (seen->n < SpanRanges::kMax) {
+            seen->lo[seen->n] = a;
+            seen->hi[seen->n++] = b;
+        }
+    }
     return FA_OK;
 }
 
@@ -123,8 +143,9 @@ bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
 
 // 4-D view (d and the axes of `dims`, `strides` elements apart) of a 2-byte (elem 0: bf16, 1: fp16) or
 // E4M3 (2) tensor, box (cw, box[0 .. 2]), rows of cw elements swizzled over their own width.
+// line: the bytes that L2 fetches together (64, 128, 256).
 int encode_view(CUtensorMap *m, const void *base, int d, const long long (&dims)[3], const long long (&strides)[3],
-                int cw, const int (&box)[3], int elem) {
+                int cw, const int (&box)[3], int elem, int line) {
     EncodeTiledFn fn = encode_fn();
     if (fn == nullptr) return FA_ERR_CUDA;
     const cuuint64_t es = elem == 2 ? 1 : 2;
@@ -137,7 +158,8 @@ int encode_view(CUtensorMap *m, const void *base, int d, const long long (&dims)
                                    : elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const CUresult r = fn(m, dt, 4, const_cast<void *>(base), gd, gs, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                          line == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
+                          : line == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
 

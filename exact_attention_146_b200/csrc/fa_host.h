@@ -65,12 +65,18 @@ int check_layout(const Span *in, int n_in, const Span *out, int n_out, Same same
     }
     return FA_OK;
 }
+// The allocations that one call's arrays have been found in.
+struct SpanRanges {
+    static constexpr int kMax = 16;
+    int n = 0;
+    uintptr_t lo[kMax], hi[kMax];
+};
 // check_device_range of every array that is not empty.
-int check_spans(const Span *s, int n, int dev);
+int check_spans(SpanRanges *seen, const Span *s, int n, int dev);
 
 // 4-D view of a strided tensor: (d, dims) with `strides` elements, box (cw, box).
 int encode_view(CUtensorMap *m, const void *base, int d, const long long (&dims)[3], const long long (&strides)[3],
-                int cw, const int (&box)[3], int elem);
+                int cw, const int (&box)[3], int elem, int line = 256);
 // 4-D view (d, H, N, B) of a [B, N, H, d] tensor, box (cw, heads, rows, 1); elem: 0 bf16,
 // 1 fp16, 2 E4M3 bytes.
 int encode_bnhd(CUtensorMap *m, const void *base, int d, int H, int N, int B, int cw, int rows, int heads = 1,

@@ -19,7 +19,15 @@ namespace {
 using namespace fa;
 using namespace fa_host;
 
-constexpr int kMaxRowWorkers = kMaxPagedCtas * 8;
+constexpr int kMaxRowWorkers = kMaxPagedCtas * 10;
+
+// The few-rows kernel's shape for each head dim.
+template <int D> struct RowShape { static constexpr int KEYS = 16, WARPS = 8; };
+template <> struct RowShape<32> { static constexpr int KEYS = 32, WARPS = 10; };
+template <> struct RowShape<64> { static constexpr int KEYS = 32, WARPS = 8; };
+template <> struct RowShape<192> { static constexpr int KEYS = 16, WARPS = 5; };
+template <> struct RowShape<256> { static constexpr int KEYS = 16, WARPS = 4; };
+template <int D, bool F16, int ROWS, bool TMA> using RowsOf = RowCfg<D, F16, RowShape<D>::KEYS, RowShape<D>::WARPS, ROWS, TMA>;
 
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
@@ -73,44 +81,6 @@ int make_ready(Kernel kern, int smem, int regs, int &state) {
     return state == 1 ? FA_OK : FA_ERR_CUDA;
 }
 
-// The kernel of few rows; fills what it adds to `p`.
-template <class C>
-int launch_rows(PagedParams &p, char *workspace, int ctas, int dev, cudaStream_t st) {
-    static int state[kMaxDevices] = {};
-    const int rc = make_ready(fa_paged_rows_kernel<C>, C::SMEM, 0, state[dev]);
-    if (rc != FA_OK) return rc;
-    p.pack = largest_divisor(p.n_rep, kRowRows);
-    p.plan.groups = p.Hq / p.pack;
-    p.plan.tpb = kRowRows / p.pack;
-    p.plan.workers = ctas * C::WARPS;
-    p.o_part = reinterpret_cast<float *>(workspace);
-    p.lse_part = reinterpret_cast<float *>(workspace + part_o_bytes(p.plan.workers, kRowRows, C::D));
-    p.jobs = reinterpret_cast<MergeJob *>(workspace + part_bytes(p.plan.workers, kRowRows, C::D));
-    fa_paged_rows_kernel<C><<<unsigned(ctas), C::THREADS, C::SMEM, st>>>(p);
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
-}
-
-template <int D, bool F16>
-int launch_rows_only(PagedParams p, char *workspace, int ctas, int dev, cudaStream_t st) {
-    const int rc = launch_rows<RowCfg<D, F16>>(p, workspace, ctas, dev, st);
-    if (rc != FA_OK) return rc;
-    return launch_after(fa_paged_merge_rows_kernel<D, F16>, unsigned(p.plan.workers - 1), 256, 0, st, p);
-}
-
-// The dense forward's tilings (fa_fwd.cu says why each).
-template <bool H> using Tile32 = TileCfg<32, 128, 2, 8, 2, 1, true, 2, H>;
-template <bool H> using Tile64 = TileCfg<64, 128, 2, 8, 2, 1, true, 2, H>;
-template <bool H> using Tile80 = TileCfg<80, 128, 2, 4, 1, 1, true, 0, H, false, false, true>;
-template <bool H> using Tile96 = TileCfg<96, 128, 2, 4, 1, 1, true, 0, H, false, false, true>;
-template <bool H> using Tile128 = TileCfg<128, 128, 2, 4, 1, 1, true, 0, H, false, false, true>;
-template <bool H> using Tile192 = TileCfg<192, 64, 2, 4, 1, 1, true, 0, H, false, false, true>;
-template <bool H> using Tile256 = TileCfg<256, 64, 1, 4, 1, 2, false, 0, H>;
-
-// What a unit of the tile kernel costs besides its key tiles (Q, the first tile's way through the
-// pipeline with nothing beside it, the epilogue), in key tiles: 7.5 us against 1.9 to 2.2 us a tile
-// (d = 128, 8 requests of up to 512 new tokens, 352 units).
-constexpr int kTileOverhead = 3;
-
 // The largest power of two, up to a key tile, that divides a page.
 int box_rows(int page, int most) {
     int g = 1;
@@ -127,8 +97,78 @@ struct View {
 
 // Chunks on the tensor cores; requests of at most `few` new tokens (few > 0) by the kernel of few rows
 // before it, in the same stream but not in its way: the tile kernel's CTAs start as the other's end.
+// The caches as the tensor maps see them: the axes after d, the nearer of head and slot first.
+View cache_view(const PagedParams &p, int Hkv) {
+    View kv{p.k, {Hkv, p.page, p.num_blocks}, {p.head_stride, p.slot_stride, p.block_stride}, {1, 1, 1}};
+    if (p.slot_first) {
+        std::swap(kv.dims[0], kv.dims[1]);
+        std::swap(kv.strides[0], kv.strides[1]);
+    }
+    return kv;
+}
+
+// Tensor maps of K and V with boxes of cw columns and `run` slots.
+int encode_cache(CUtensorMap *mk, CUtensorMap *mv, const PagedParams &p, View kv, int d, int cw, int run, bool f16) {
+    kv.box[p.slot_first ? 0 : 1] = run;
+    // L2 fetches no more at once than lies in the row, where the bytes behind it are another head's: those are
+    // read at other times by other workers (d = 80, 48 requests: 160-byte rows fetched as whole lines took 1.6 times the bytes).
+    const int row = 2 * d, line = p.slot_stride == d || row % 256 == 0 ? 256 : row % 128 == 0 ? 128 : 64;
+    const int rc = encode_view(mk, p.k, d, kv.dims, kv.strides, cw, kv.box, f16 ? 1 : 0, line);
+    return rc != FA_OK ? rc : encode_view(mv, p.v, d, kv.dims, kv.strides, cw, kv.box, f16 ? 1 : 0, line);
+}
+
+// The kernel of few rows; fills what it adds to `p`.
 template <class C>
-int launch_tiles(const PagedParams &base, const View &q, View kv, const void *v, int few, char *workspace, int ctas, int dev,
+int launch_rows_as(PagedParams &p, const View &kv, char *workspace, int ctas, int dev, cudaStream_t st) {
+    static int state[kMaxDevices] = {};
+    int rc = make_ready(fa_paged_rows_kernel<C>, C::SMEM, 0, state[dev]);
+    if (rc != FA_OK) return rc;
+    CUtensorMap mk{}, mv{};
+    if (C::TMA) {
+        p.run = box_rows(p.page, C::KEYS);
+        if ((rc = encode_cache(&mk, &mv, p, kv, C::D, C::CW, p.run, C::F16)) != FA_OK) return rc;
+    }
+    p.pack = largest_divisor(p.n_rep, C::ROWS);
+    p.plan.groups = p.Hq / p.pack;
+    p.plan.tpb = C::ROWS / p.pack;
+    p.plan.workers = ctas * C::WARPS;
+    p.o_part = reinterpret_cast<float *>(workspace);
+    p.lse_part = reinterpret_cast<float *>(workspace + part_o_bytes(p.plan.workers, C::ROWS, C::D));
+    p.jobs = reinterpret_cast<MergeJob *>(workspace + part_bytes(p.plan.workers, C::ROWS, C::D));
+    fa_paged_rows_kernel<C><<<unsigned(ctas), C::THREADS, C::SMEM, st>>>(mk, mv, p);
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+// Pages of whole swizzle atoms come by TMA, any other row by row.
+template <int D, bool F16, int ROWS>
+int launch_rows(PagedParams &p, const View &kv, char *workspace, int ctas, int dev, cudaStream_t st) {
+    return p.page % 8 == 0 && p.num_blocks > 0 ? launch_rows_as<RowsOf<D, F16, ROWS, true>>(p, kv, workspace, ctas, dev, st)
+                                               : launch_rows_as<RowsOf<D, F16, ROWS, false>>(p, kv, workspace, ctas, dev, st);
+}
+
+template <int D, bool F16, int ROWS>
+int launch_rows_only(PagedParams p, const View &kv, char *workspace, int ctas, int dev, cudaStream_t st) {
+    const int rc = launch_rows<D, F16, ROWS>(p, kv, workspace, ctas, dev, st);
+    if (rc != FA_OK) return rc;
+    return launch_after(fa_paged_merge_rows_kernel<D, F16, ROWS>, unsigned(p.plan.workers - 1), 256, 0, st, p);
+}
+
+// The dense forward's tilings (fa_fwd.cu says why each).
+template <bool H> using Tile32 = TileCfg<32, 128, 2, 8, 2, 1, true, 2, H>;
+template <bool H> using Tile64 = TileCfg<64, 128, 2, 8, 2, 1, true, 2, H>;
+template <bool H> using Tile80 = TileCfg<80, 128, 2, 4, 1, 1, true, 0, H, false, false, true>;
+template <bool H> using Tile96 = TileCfg<96, 128, 2, 4, 1, 1, true, 0, H, false, false, true>;
+template <bool H> using Tile128 = TileCfg<128, 128, 2, 4, 1, 1, true, 0, H, false, false, true>;
+template <bool H> using Tile192 = TileCfg<192, 64, 2, 4, 1, 1, true, 0, H, false, false, true>;
+template <bool H> using Tile256 = TileCfg<256, 64, 1, 4, 1, 2, false, 0, H>;
+
+// What a unit of the tile kernel costs besides its key tiles (Q, the first tile's way through the
+// pipeline with nothing beside it, the epilogue), in key tiles: 7.5 us against 1.9 to 2.2 us a tile
+// (d = 128, 8 requests of up to 512 new tokens, 352 units).
+constexpr int kTileOverhead = 3;
+
+template <class C>
+int launch_tiles(const PagedParams &base, const View &q, const View &kv, int few, char *workspace, int ctas, int dev,
                  cudaStream_t st) {
     static int state[kMaxDevices] = {};
     // the register split inside the kernel counts on exactly this launch budget
@@ -142,9 +182,7 @@ int launch_tiles(const PagedParams &base, const View &q, View kv, const void *v,
     p.plan.workers = ctas;
     p.plan.overhead = kTileOverhead;
     p.plan.n_lo = few + 1;
-    p.box_rows = box_rows(p.page, C::BC);
-    p.slot_first = p.slot_stride < p.head_stride ? 1 : 0;
-    kv.box[p.slot_first ? 0 : 1] = p.box_rows;
+    p.run = box_rows(p.page, C::BC);
     constexpr int rows = C::NQT * kBlockQ;
     char *const ws = workspace + part_bytes(kMaxRowWorkers, kRowRows, C::D) + job_bytes(kMaxRowWorkers);
     p.o_part = reinterpret_cast<float *>(ws);
@@ -154,12 +192,11 @@ int launch_tiles(const PagedParams &base, const View &q, View kv, const void *v,
     CUtensorMap mq, mk, mv;
     const int elem = C::F16 ? 1 : 0;
     if ((rc = encode_view(&mq, q.base, C::D, q.dims, q.strides, C::CW, q.box, elem)) != FA_OK) return rc;
-    if ((rc = encode_view(&mk, kv.base, C::D, kv.dims, kv.strides, C::CW, kv.box, elem)) != FA_OK) return rc;
-    if ((rc = encode_view(&mv, v, C::D, kv.dims, kv.strides, C::CW, kv.box, elem)) != FA_OK) return rc;
+    if ((rc = encode_cache(&mk, &mv, p, kv, C::D, C::CW, p.run, C::F16)) != FA_OK) return rc;
     PagedParams pf = base;
     pf.plan.n_hi = few;
     pf.say = 0;
-    if (few > 0 && (rc = launch_rows<RowCfg<C::D, C::F16>>(pf, workspace, ctas, dev, st)) != FA_OK) return rc;
+    if (few > 0 && (rc = launch_rows<C::D, C::F16, kRowRows>(pf, kv, workspace, ctas, dev, st)) != FA_OK) return rc;
     if (few > 0) {   // beside the kernel before it, which began when the inputs were complete
         rc = launch_after(fa_paged_tiles_kernel<C>, unsigned(ctas), C::THREADS, PlanSmem<C>::BYTES, st, mq, mk, mv, p);
         if (rc != FA_OK) return rc;
@@ -173,35 +210,30 @@ int launch_tiles(const PagedParams &base, const View &q, View kv, const void *v,
 }
 
 template <bool F16>
-int dispatch_tiles(PagedParams p, int d, int num_blocks, int Hkv, int few, char *workspace, int ctas, int dev, cudaStream_t st) {
+int dispatch_tiles(PagedParams p, const View &kv, int d, int few, char *workspace, int ctas, int dev, cudaStream_t st) {
     p.pack = largest_divisor(p.n_rep, kBlockQ);
     const View q{p.q, {p.Hq, p.plan.T, 1}, {d, p.q_stride, p.q_stride * p.plan.T}, {p.pack, kBlockQ / p.pack, 1}};
-    View kv{p.k, {Hkv, p.page, num_blocks}, {p.head_stride, p.slot_stride, p.block_stride}, {1, 1, 1}};
-    if (p.slot_stride < p.head_stride) {
-        std::swap(kv.dims[0], kv.dims[1]);
-        std::swap(kv.strides[0], kv.strides[1]);
-    }
     switch (d) {
-        case 32: return launch_tiles<Tile32<F16>>(p, q, kv, p.v, few, workspace, ctas, dev, st);
-        case 64: return launch_tiles<Tile64<F16>>(p, q, kv, p.v, few, workspace, ctas, dev, st);
-        case 80: return launch_tiles<Tile80<F16>>(p, q, kv, p.v, few, workspace, ctas, dev, st);
-        case 96: return launch_tiles<Tile96<F16>>(p, q, kv, p.v, few, workspace, ctas, dev, st);
-        case 128: return launch_tiles<Tile128<F16>>(p, q, kv, p.v, few, workspace, ctas, dev, st);
-        case 192: return launch_tiles<Tile192<F16>>(p, q, kv, p.v, few, workspace, ctas, dev, st);
-        default: return launch_tiles<Tile256<F16>>(p, q, kv, p.v, few, workspace, ctas, dev, st);
+        case 32: return launch_tiles<Tile32<F16>>(p, q, kv, few, workspace, ctas, dev, st);
+        case 64: return launch_tiles<Tile64<F16>>(p, q, kv, few, workspace, ctas, dev, st);
+        case 80: return launch_tiles<Tile80<F16>>(p, q, kv, few, workspace, ctas, dev, st);
+        case 96: return launch_tiles<Tile96<F16>>(p, q, kv, few, workspace, ctas, dev, st);
+        case 128: return launch_tiles<Tile128<F16>>(p, q, kv, few, workspace, ctas, dev, st);
+        case 192: return launch_tiles<Tile192<F16>>(p, q, kv, few, workspace, ctas, dev, st);
+        default: return launch_tiles<Tile256<F16>>(p, q, kv, few, workspace, ctas, dev, st);
     }
 }
 
-template <bool F16>
-int dispatch_rows(const PagedParams &p, int d, char *workspace, int ctas, int dev, cudaStream_t st) {
+template <bool F16, int ROWS>
+int dispatch_rows(const PagedParams &p, const View &kv, int d, char *workspace, int ctas, int dev, cudaStream_t st) {
     switch (d) {
-        case 32: return launch_rows_only<32, F16>(p, workspace, ctas, dev, st);
-        case 64: return launch_rows_only<64, F16>(p, workspace, ctas, dev, st);
-        case 80: return launch_rows_only<80, F16>(p, workspace, ctas, dev, st);
-        case 96: return launch_rows_only<96, F16>(p, workspace, ctas, dev, st);
-        case 128: return launch_rows_only<128, F16>(p, workspace, ctas, dev, st);
-        case 192: return launch_rows_only<192, F16>(p, workspace, ctas, dev, st);
-        default: return launch_rows_only<256, F16>(p, workspace, ctas, dev, st);
+        case 32: return launch_rows_only<32, F16, ROWS>(p, kv, workspace, ctas, dev, st);
+        case 64: return launch_rows_only<64, F16, ROWS>(p, kv, workspace, ctas, dev, st);
+        case 80: return launch_rows_only<80, F16, ROWS>(p, kv, workspace, ctas, dev, st);
+        case 96: return launch_rows_only<96, F16, ROWS>(p, kv, workspace, ctas, dev, st);
+        case 128: return launch_rows_only<128, F16, ROWS>(p, kv, workspace, ctas, dev, st);
+        case 192: return launch_rows_only<192, F16, ROWS>(p, kv, workspace, ctas, dev, st);
+        default: return launch_rows_only<256, F16, ROWS>(p, kv, workspace, ctas, dev, st);
     }
 }
 
@@ -235,7 +267,8 @@ int paged_fwd(const void *q, long long q_stride, const fa_paged_cache *cache, co
     DeviceState *dev = nullptr;
     int dev_id = -1;
     if ((rc = current_device(&dev, &dev_id)) != FA_OK) return rc;
-    if ((rc = check_spans(in, 6, dev_id)) != FA_OK || (rc = check_spans(outs, 3, dev_id)) != FA_OK) return rc;
+    SpanRanges seen;
+    if ((rc = check_spans(&seen, in, 6, dev_id)) != FA_OK || (rc = check_spans(&seen, outs, 3, dev_id)) != FA_OK) return rc;
 
     PagedParams p{};
     p.plan.cu = cu_seqlens;
@@ -268,16 +301,22 @@ int paged_fwd(const void *q, long long q_stride, const fa_paged_cache *cache, co
     p.plan.n_lo = 1;
     p.plan.n_hi = max_new;
     p.say = 1;
+    p.slot_first = p.slot_stride < p.head_stride ? 1 : 0;
+    const View kv = cache_view(p, Hkv);
     char *const ws = static_cast<char *>(workspace);
     // Row tiles of 128 need pages of whole swizzle atoms (8 slots); any other page, and calls of few rows,
     // take the kernel that gathers key by key.  In a mixed call the requests of few rows take it too.
     const int few = kRowRows / p.n_rep;   // new tokens whose rows fit it
     if (max_new > few && p.page % 8 == 0 && p.num_blocks > 0) {
         const int split = R > 1 ? few : 0;
-        return f16 ? dispatch_tiles<true>(p, d, p.num_blocks, Hkv, split, ws, ctas, dev_id, st)
-                   : dispatch_tiles<false>(p, d, p.num_blocks, Hkv, split, ws, ctas, dev_id, st);
+        return f16 ? dispatch_tiles<true>(p, kv, d, split, ws, ctas, dev_id, st)
+                   : dispatch_tiles<false>(p, kv, d, split, ws, ctas, dev_id, st);
     }
-    return f16 ? dispatch_rows<true>(p, d, ws, ctas, dev_id, st) : dispatch_rows<false>(p, d, ws, ctas, dev_id, st);
+    // Rows are the narrow side of the kernel's products: 8 where they fit (a decoding step of up to 8 heads a KV
+    // head), which halves the products.
+    if ((long long)max_new * p.n_rep <= 8)
+        return f16 ? dispatch_rows<true, 8>(p, kv, d, ws, ctas, dev_id, st) : dispatch_rows<false, 8>(p, kv, d, ws, ctas, dev_id, st);
+    return f16 ? dispatch_rows<true, kRowRows>(p, kv, d, ws, ctas, dev_id, st) : dispatch_rows<false, kRowRows>(p, kv, d, ws, ctas, dev_id, st);
 }
 
 }  // namespace

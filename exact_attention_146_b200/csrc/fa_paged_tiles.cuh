@@ -22,8 +22,6 @@ namespace fa {
 
 struct PagedTileParams : PagedParams {
     int tq;            // tokens a row tile: 128 / pack
-    int box_rows;      // slots a K/V box
-    int slot_first;    // the tensor map's second axis is the slot (else the head)
     long long *cuts;   // workspace: the cuts of the line, each CTA's copy (kMaxPagedCtas + 1 places)
 };
 
@@ -182,7 +180,7 @@ __device__ void paged_producer_role(const CUtensorMap *tm_q, const CUtensorMap *
     sm100::prefetch_tensormap(tm_k);
     sm100::prefetch_tensormap(tm_v);
     const int lane = int(threadIdx.x) % 32;
-    const int boxes = C::BC / p.box_rows;
+    const int boxes = C::BC / p.run;
     const uint32_t q_bytes = uint32_t(C::NCH * C::RB * p.tq * p.pack);
     uint32_t kv_cnt = 0;
     uint32_t qcnt[2] = {0, 0};
@@ -194,15 +192,15 @@ __device__ void paged_producer_role(const CUtensorMap *tm_q, const CUtensorMap *
         const int *table = p.table + w.r * p.table_stride;
         // Block and slot of box `lane` of key tile j (a block past the cache: zeros).
         auto find_box = [&](int j, int &block, int &slot) {
-            const int key = j * C::BC + lane * p.box_rows;
-            const bool seen = lane < boxes && key <= w.hi && key + p.box_rows > w.lo;
+            const int key = j * C::BC + lane * p.run;
+            const bool seen = lane < boxes && key <= w.hi && key + p.run > w.lo;
             const int page = seen ? key / p.page : 0;
             slot = seen ? key - page * p.page : 0;
             block = seen ? __ldg(table + page) : p.num_blocks;
         };
         auto slot_named = [&](int j) {   // the table was asked for this box
-            const int key = j * C::BC + lane * p.box_rows;
-            return lane < boxes && key <= w.hi && key + p.box_rows > w.lo;
+            const int key = j * C::BC + lane * p.run;
+            return lane < boxes && key <= w.hi && key + p.run > w.lo;
         };
         int block, slot;
         find_box(w.j_lo, block, slot);
@@ -243,7 +241,7 @@ __device__ void paged_producer_role(const CUtensorMap *tm_q, const CUtensorMap *
                     const int c1 = p.slot_first ? sl : kvh, c2 = p.slot_first ? kvh : sl;
 #pragma unroll
                     for (int c = 0; c < C::NCH; ++c)
-                        sm100::tma_load_4d_elected(dst + uint32_t(c * C::KV_CHUNK + i * p.box_rows * C::RB), m, fb, c * C::CW, c1, c2, b);
+                        sm100::tma_load_4d_elected(dst + uint32_t(c * C::KV_CHUNK + i * p.run * C::RB), m, fb, c * C::CW, c1, c2, b);
                 }
                 ++kv_cnt;
             }
@@ -455,10 +453,10 @@ fa_paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 
     if (warp < C::SOFTMAX_WARPS) {
         if constexpr (C::REALLOC_REGS) sm100::regs_increase<C::SOFTMAX_REGS>();
-        paged_softmax_role<C>(p, PagedUnits<C, kRoleSoftmax>{sbase, smem, ctl, p.box_rows, 0}, sbase, tmem, ctl, warp, lane);
+        paged_softmax_role<C>(p, PagedUnits<C, kRoleSoftmax>{sbase, smem, ctl, p.run, 0}, sbase, tmem, ctl, warp, lane);
     } else {
         if constexpr (C::REALLOC_REGS) sm100::regs_decrease<C::CONTROL_REGS>();
-        const PagedUnits<C, kRoleControl> units{sbase, smem, ctl, p.box_rows, 0};
+        const PagedUnits<C, kRoleControl> units{sbase, smem, ctl, p.run, 0};
         if (warp == C::TMA_WARP) paged_producer_role<C>(&tm_q, &tm_k, &tm_v, p, units, sbase, ctl);
         else if (warp == C::MMA_WARP) mma_role<C>(units, sbase, tmem, ctl);
         else if (warp == C::MMA_WARP + 1)
@@ -482,11 +480,12 @@ __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_consta
     const int tile_blocks = (p.plan.workers - 1) * kPer, i = int(blockIdx.x);
     asm volatile("griddepcontrol.wait;" ::: "memory");   // the pieces, cuts and jobs are written
     if (i < tile_blocks) {
-        const int w = i / kPer + 1, row0 = i % kPer * 32;
-        merge_unit<C::D, C::F16, kRows, kBlockQ>(p, w, row0, row0 + 32,
-                                                 [&](int s) { return p.cuts[w - 1 + s] < p.cuts[w + s]; });
+        const int w = i / kPer + 1;
+        const MergeJob job = p.jobs[w];
+        if (job.parts > 0)
+            merge_unit<C::D, C::F16, kRows, kBlockQ>(p, job, w, i % kPer * 32, 32, [&](int s) { return p.cuts[w - 1 + s] < p.cuts[w + s]; });
     } else {
-        merge_unit<C::D, C::F16, kRowRows, kRowRows>(few, i - tile_blocks + 1, 0, kRowRows, [](int) { return true; });
+        merge_rows<C::D, C::F16, kRowRows>(few, i - tile_blocks + 1);
     }
 }
 

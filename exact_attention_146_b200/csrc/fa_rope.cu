@@ -309,7 +309,8 @@ int rope(const void *q, long long q_stride, void *q_out, long long qo_stride, in
     DeviceState *dev = nullptr;
     int dev_id = -1;
     if ((rc = current_device(&dev, &dev_id)) != FA_OK) return rc;
-    if ((rc = check_spans(in, 3, dev_id)) != FA_OK || (rc = check_spans(out, 2, dev_id)) != FA_OK) return rc;
+    SpanRanges seen;
+    if ((rc = check_spans(&seen, in, 3, dev_id)) != FA_OK || (rc = check_spans(&seen, out, 2, dev_id)) != FA_OK) return rc;
     RopeParams p{};
     p.q = static_cast<const uint16_t *>(q);
     p.k = static_cast<const uint16_t *>(k);
@@ -370,7 +371,8 @@ int rope_append(const void *q, long long q_stride, void *q_out, long long qo_str
     DeviceState *dev = nullptr;
     int dev_id = -1;
     if ((rc = current_device(&dev, &dev_id)) != FA_OK) return rc;
-    if ((rc = check_spans(in, 5, dev_id)) != FA_OK || (rc = check_spans(out, 3, dev_id)) != FA_OK) return rc;
+    SpanRanges seen;
+    if ((rc = check_spans(&seen, in, 5, dev_id)) != FA_OK || (rc = check_spans(&seen, out, 3, dev_id)) != FA_OK) return rc;
     RopeParams p{};
     p.q = static_cast<const uint16_t *>(q);
     p.k = static_cast<const uint16_t *>(k);

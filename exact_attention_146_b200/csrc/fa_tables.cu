@@ -314,7 +314,8 @@ int fa_kv_reserve(const int *ctx_lens, const int *new_lens, int R, int *block_ta
     DeviceState *dev = nullptr;
     int dev_id = -1;
     if ((rc = current_device(&dev, &dev_id)) != FA_OK) return rc;
-    if ((rc = check_spans(in, 4, dev_id)) != FA_OK || (rc = check_spans(out, 6, dev_id)) != FA_OK) return rc;
+    SpanRanges seen;
+    if ((rc = check_spans(&seen, in, 4, dev_id)) != FA_OK || (rc = check_spans(&seen, out, 6, dev_id)) != FA_OK) return rc;
     ReserveParams p{};
     p.ctx = ctx_lens;
     p.fresh = new_lens;
@@ -356,7 +357,8 @@ int fa_kv_release(const int *lens, const int *done, int R, const int *block_tabl
     DeviceState *dev = nullptr;
     int dev_id = -1;
     if ((rc = current_device(&dev, &dev_id)) != FA_OK) return rc;
-    if ((rc = check_spans(in, 4, dev_id)) != FA_OK || (rc = check_spans(out, 3, dev_id)) != FA_OK) return rc;
+    SpanRanges seen;
+    if ((rc = check_spans(&seen, in, 4, dev_id)) != FA_OK || (rc = check_spans(&seen, out, 3, dev_id)) != FA_OK) return rc;
     ReleaseParams p{};
     p.lens = lens;
     p.done = done;

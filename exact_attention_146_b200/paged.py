@@ -43,21 +43,36 @@ def declare(L) -> None:
     L.fa_paged_workspace_bytes.restype = ctypes.c_size_t
 
 
-def _core():
+class _Types:
+    """torch's types and stream query, looked up at the first call (the module imports without torch)."""
+    ready = False
+
+
+def _init() -> None:
+    import torch
+
     import exact_attention_146_b200 as fa
-    return fa
+    _Types.i32, _Types.i64, _Types.f32 = torch.int32, torch.int64, torch.float32
+    _Types.half = {torch.bfloat16: "", torch.float16: "_f16"}
+    _Types.torch, _Types.fa = torch, fa
+    # the current stream's handle without building a Stream object (3 us a call)
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+    _Types.current = (lambda: raw(device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
+    L = fa.lib()
+    _Types.call = {n: getattr(L, n) for n in ("fa_kv_reserve", "fa_kv_release", "fa_rope", "fa_rope_f16", "fa_rope_append",
+                                              "fa_rope_append_f16", "fa_paged_fwd", "fa_paged_fwd_f16")}
+    _Types.ready = True
 
 
 def _run(name, stream, *args):
-    fa = _core()
-    rc = getattr(fa.lib(), name)(*args, fa._stream_handle(stream))
-    if rc != fa.FA_OK:
-        raise fa.FaError(rc, name)
+    rc = _Types.call[name](*args, _Types.current() if stream is None else _Types.fa._stream_handle(stream))
+    if rc != 0:
+        raise _Types.fa.FaError(rc, name)
 
 
 def _empty(shape, dtype, device, stream):
     """A buffer made here for a call on `stream` (None: the current one)."""
-    import torch
+    torch = _Types.torch
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
@@ -66,48 +81,53 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _ints(name, t, shape, dtype=None):
-    import torch
-    dtype = dtype or torch.int32
-    if t.dtype != dtype or not t.is_cuda or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    return t
+def _ints(name, t, n, dtype=None):
+    """The pointer of a contiguous 1-D CUDA tensor of n int32 (or dtype)."""
+    dtype = dtype or _Types.i32
+    if t.dtype is not dtype or not t.is_cuda or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor ({n},), got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _table(t, R):
-    import torch
-    if t.dtype != torch.int32 or not t.is_cuda or t.dim() != 2 or t.shape[0] != R or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"block_table must be an int32 CUDA tensor [{R}, max_blocks] with adjacent entries, got {t.dtype} {tuple(t.shape)}")
-    width = t.shape[1]
-    return t, (max(t.stride(0), width) if R > 1 else width), width
+    """(pointer, entries from row to row, entries a row) of a block table."""
+    if t.dtype is _Types.i32 and t.is_cuda and t.dim() == 2:
+        rows, width = t.shape
+        if rows == R and (width <= 1 or t.stride(1) == 1):
+            return t.data_ptr(), (max(t.stride(0), width) if R > 1 else width), width
+    raise ValueError(f"block_table must be an int32 CUDA tensor [{R}, max_blocks] with adjacent entries, got {t.dtype} {tuple(t.shape)}")
 
 
-def _rows(name, t, dtype, d=None):
+def _rows(name, t, dtype, shape=None):
     """A [T, heads, d] tensor whose heads lie next to each other: (pointer, elements from token to token)."""
-    if t.dtype != dtype or not t.is_cuda or t.dim() != 3 or (d is not None and t.shape[2] != d):
-        raise ValueError(f"{name} must be a {dtype} CUDA tensor [T, heads, d], got {t.dtype} {tuple(t.shape)}")
-    T, H, dd = t.shape
-    if (dd > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != dd):
-        raise ValueError(f"{name}: the heads of a token must lie next to each other, strides {tuple(t.stride())}")
-    return t.data_ptr(), (t.stride(0) if T > 1 else H * dd)
+    if t.dtype is not dtype or not t.is_cuda or t.dim() != 3 or (shape is not None and t.shape != shape):
+        want = "[T, heads, d]" if shape is None else tuple(shape)
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor {want}, got {t.dtype} {tuple(t.shape)}")
+    T, H, d = t.shape
+    step, head, one = t.stride()
+    if (d > 1 and one != 1) or (H > 1 and head != d):
+        raise ValueError(f"{name}: the heads of a token must lie next to each other, strides {t.stride()}")
+    return t.data_ptr(), (step if T > 1 else H * d)
 
 
 def _cache(k, v):
     """The C description of k and v caches, logically [blocks, slots, heads, d] with any strides of the first three."""
+    shape, strides = k.shape, k.stride()
     for name, t in (("k_cache", k), ("v_cache", v)):
-        if not t.is_cuda or t.dim() != 4 or t.dtype != k.dtype or (t.shape[3] > 1 and t.stride(3) != 1):
+        if not t.is_cuda or len(shape) != 4 or t.dtype is not k.dtype or (shape[3] > 1 and strides[3] != 1):
             raise ValueError(f"{name} must be a 4-D CUDA tensor [blocks, slots, heads, d] with adjacent elements, got {t.dtype} {tuple(t.shape)}")
-    if k.shape != v.shape or k.stride() != v.stride():
-        raise ValueError(f"k_cache and v_cache must have the same shape and strides, got {tuple(k.shape)} {k.stride()} and {tuple(v.shape)} {v.stride()}")
-    blocks, page, heads, d = k.shape
-    return _Cache(k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2), blocks, page, heads, d)
+    if shape != v.shape or strides != v.stride():
+        raise ValueError(f"k_cache and v_cache must have the same shape and strides, got {tuple(shape)} {strides} and {tuple(v.shape)} {v.stride()}")
+    return _Cache(k.data_ptr(), v.data_ptr(), strides[0], strides[1], strides[2], shape[0], shape[1], shape[2], shape[3])
 
 
 def _half(t):
-    import torch
-    if t.dtype not in (torch.bfloat16, torch.float16):
+    """The suffix of the entry points for t's type."""
+    if not _Types.ready:
+        _init()
+    if t.dtype not in _Types.half:
         raise ValueError(f"bf16 or fp16 expected, got {t.dtype}")
-    return "_f16" if t.dtype == torch.float16 else ""
+    return _Types.half[t.dtype]
 
 
 class RopeTable:
@@ -124,21 +144,22 @@ class RopeTable:
         self.rot_dim = 2 * len(inv)
         self.num_axes = max(axes, default=0) + 1
         self.interleaved = bool(interleaved)
+        self._specs = {}
         self._inv = (ctypes.c_double * max(1, len(inv)))(*inv)
         self._axis = (ctypes.c_int * max(1, len(inv)))(*axes)
 
     def _spec(self, positions, T):
-        import torch
-        if positions.dim() == 1:
-            positions = positions[None]
-        n = positions.shape[0]
-        if positions.dtype != torch.int32 or not positions.is_cuda or positions.dim() != 2 or positions.shape[1] != T or \
-                (T > 1 and positions.stride(1) != 1):
+        """(spec, pointer, elements from axis to axis) of positions [axes, T] or [T]."""
+        n, step = (positions.shape[0], positions.stride(0)) if positions.dim() == 2 else (1, T)
+        if positions.dtype is not _Types.i32 or not positions.is_cuda or positions.dim() not in (1, 2) or \
+                positions.shape[-1] != T or (T > 1 and positions.stride(-1) != 1):
             raise ValueError(f"positions must be int32 CUDA [axes, {T}] (or [{T}]), got {positions.dtype} {tuple(positions.shape)}")
         if n < self.num_axes:
             raise ValueError(f"the table uses {self.num_axes} axes, positions has {n}")
-        spec = _RopeSpec(self.rot_dim, int(self.interleaved), n, self._inv, self._axis)
-        return spec, positions, (max(positions.stride(0), T) if n > 1 else T)
+        spec = self._specs.get(n)
+        if spec is None:
+            spec = self._specs[n] = ctypes.byref(_RopeSpec(self.rot_dim, int(self.interleaved), n, self._inv, self._axis))
+        return spec, positions.data_ptr(), (max(step, T) if n > 1 else T)
 
 
 def fa_rope(q, positions, table: RopeTable, *, k=None, inverse: bool = False, q_out=None, k_out=None, stream=None):
@@ -146,28 +167,26 @@ def fa_rope(q, positions, table: RopeTable, *, k=None, inverse: bool = False, q_
     inverse = True is its gradient (the opposite turn).  q and k may be slices of one projection.
     Returns (q_out, k_out), or q_out alone without k; q_out may be q and k_out k (in place)."""
     f16 = _half(q)
-    T, Hq, d = q.shape
-    qp, qs = _rows("q", q, q.dtype)
+    dtype = q.dtype
+    qp, qs = _rows("q", q, dtype)
+    shape = q.shape
+    T, Hq, d = shape
     if q_out is None:
-        q_out = _empty((T, Hq, d), q.dtype, q.device, stream)
-    if tuple(q_out.shape) != (T, Hq, d):
-        raise ValueError(f"q_out must be {(T, Hq, d)}, got {tuple(q_out.shape)}")
-    qo, qos = _rows("q_out", q_out, q.dtype, d)
+        q_out = _empty(shape, dtype, q.device, stream)
+    qo, qos = _rows("q_out", q_out, dtype, shape)
     kp = ko = None
     ks = kos = Hkv = 0
     if k is not None:
-        if k.dim() != 3 or k.shape[0] != T:
-            raise ValueError(f"k must be [{T}, heads, {d}], got {tuple(k.shape)}")
-        kp, ks = _rows("k", k, q.dtype, d)
-        Hkv = k.shape[1]
+        kp, ks = _rows("k", k, dtype)
+        shape = k.shape
+        Hkv = shape[1]
+        if shape[0] != T or shape[2] != d:
+            raise ValueError(f"k must be [{T}, heads, {d}], got {tuple(shape)}")
         if k_out is None:
-            k_out = _empty((T, Hkv, d), q.dtype, q.device, stream)
-        if tuple(k_out.shape) != (T, Hkv, d):
-            raise ValueError(f"k_out must be {(T, Hkv, d)}, got {tuple(k_out.shape)}")
-        ko, kos = _rows("k_out", k_out, q.dtype, d)
+            k_out = _empty(shape, dtype, q.device, stream)
+        ko, kos = _rows("k_out", k_out, dtype, shape)
     spec, pos, ps = table._spec(positions, T)
-    _run("fa_rope" + f16, stream, qp, qs, qo, qos, Hq, kp, ks, ko, kos, Hkv, T, d, pos.data_ptr(), ps, ctypes.byref(spec),
-         int(bool(inverse)))
+    _run("fa_rope" + f16, stream, qp, qs, qo, qos, Hq, kp, ks, ko, kos, Hkv, T, d, pos, ps, spec, 1 if inverse else 0)
     return q_out if k is None else (q_out, k_out)
 
 
@@ -176,29 +195,27 @@ def fa_rope_append(q, k, v, positions, table: RopeTable, k_cache, v_cache, slots
     (int64, block * page_size + slot; negative: the row is left out) of the caches, logically
     [blocks, slots, Hkv, d].  q may be None.  Returns q_out (rows without a slot as they were)."""
     f16 = _half(k)
+    dtype = k.dtype
+    kp, ks = _rows("k", k, dtype)
+    vp, vs = _rows("v", v, dtype, k.shape)
     T, Hkv, d = k.shape
-    kp, ks = _rows("k", k, k.dtype)
-    vp, vs = _rows("v", v, k.dtype, d)
     c = _cache(k_cache, v_cache)
-    if v.shape != k.shape or (c.Hkv, c.d) != (Hkv, d) or k_cache.dtype != k.dtype:
-        raise ValueError(f"shape mismatch k{tuple(k.shape)} v{tuple(v.shape)} cache{tuple(k_cache.shape)} {k_cache.dtype}")
-    import torch
-    _ints("slots", slots, (T,), torch.int64)
+    if (c.Hkv, c.d) != (Hkv, d) or k_cache.dtype is not dtype:
+        raise ValueError(f"shape mismatch k{tuple(k.shape)} {dtype} cache{tuple(k_cache.shape)} {k_cache.dtype}")
     qp = qo = None
     qs = qos = Hq = 0
     if q is not None:
-        if q.dim() != 3 or q.shape[0] != T:
-            raise ValueError(f"q must be [{T}, heads, {d}], got {tuple(q.shape)}")
-        qp, qs = _rows("q", q, k.dtype, d)
-        Hq = q.shape[1]
+        qp, qs = _rows("q", q, dtype)
+        shape = q.shape
+        Hq = shape[1]
+        if shape[0] != T or shape[2] != d:
+            raise ValueError(f"q must be [{T}, heads, {d}], got {tuple(shape)}")
         if q_out is None:
-            q_out = _empty((T, Hq, d), q.dtype, q.device, stream)
-        if tuple(q_out.shape) != (T, Hq, d):
-            raise ValueError(f"q_out must be {(T, Hq, d)}, got {tuple(q_out.shape)}")
-        qo, qos = _rows("q_out", q_out, k.dtype, d)
+            q_out = _empty(shape, dtype, q.device, stream)
+        qo, qos = _rows("q_out", q_out, dtype, shape)
     spec, pos, ps = table._spec(positions, T)
-    _run("fa_rope_append" + f16, stream, qp, qs, qo, qos, Hq, kp, ks, vp, vs, T, pos.data_ptr(), ps, ctypes.byref(spec),
-         ctypes.byref(c), slots.data_ptr())
+    _run("fa_rope_append" + f16, stream, qp, qs, qo, qos, Hq, kp, ks, vp, vs, T, pos, ps, spec, ctypes.byref(c),
+         _ints("slots", slots, T, _Types.i64))
     return q_out if q is not None else None
 
 
@@ -208,26 +225,30 @@ def fa_kv_reserve(ctx_lens, new_lens, block_table, free_blocks, free_count, *, p
     block_table [R, max_blocks] and returns (cu_seqlens [R + 1], seq_lens [R], positions [T], slots [T]
     int64, free_count_out [1]).  T is given by num_tokens, or by positions or slots.  seq_lens may be
     ctx_lens and free_count_out free_count (updated in place)."""
-    import torch
-    R = ctx_lens.shape[0]
-    _ints("ctx_lens", ctx_lens, (R,))
-    _ints("new_lens", new_lens, (R,))
+    if not _Types.ready:
+        _init()
+    R = ctx_lens.numel()
+    given = positions if positions is not None else slots
+    if num_tokens is None and given is None:
+        raise ValueError("num_tokens, or positions or slots of that length, must be given")
+    T = given.numel() if num_tokens is None else int(num_tokens)
+    dev, i32 = ctx_lens.device, _Types.i32
+    if cu_seqlens is None:
+        cu_seqlens = _empty((R + 1,), i32, dev, stream)
+    if seq_lens is None:
+        seq_lens = _empty((R,), i32, dev, stream)
+    if positions is None:
+        positions = _empty((T,), i32, dev, stream)
+    if slots is None:
+        slots = _empty((T,), _Types.i64, dev, stream)
+    if free_count_out is None:
+        free_count_out = _empty((1,), i32, dev, stream)
     table, stride, width = _table(block_table, R)
-    _ints("free_blocks", free_blocks, (free_blocks.numel(),))
-    _ints("free_count", free_count, (1,))
-    given = [int(t.numel()) for t in (positions, slots) if t is not None]
-    T = int(num_tokens) if num_tokens is not None else (given[0] if given else None)
-    if T is None or any(n != T for n in given):
-        raise ValueError("num_tokens, or positions and slots of that length, must be given")
-    dev = ctx_lens.device
-    cu_seqlens = _empty((R + 1,), torch.int32, dev, stream) if cu_seqlens is None else _ints("cu_seqlens", cu_seqlens, (R + 1,))
-    seq_lens = _empty((R,), torch.int32, dev, stream) if seq_lens is None else _ints("seq_lens", seq_lens, (R,))
-    positions = _empty((T,), torch.int32, dev, stream) if positions is None else _ints("positions", positions, (T,))
-    slots = _empty((T,), torch.int64, dev, stream) if slots is None else _ints("slots", slots, (T,), torch.int64)
-    free_count_out = _empty((1,), torch.int32, dev, stream) if free_count_out is None else _ints("free_count_out", free_count_out, (1,))
-    _run("fa_kv_reserve", stream, ctx_lens.data_ptr(), new_lens.data_ptr(), R, table.data_ptr(), stride, width,
-         free_blocks.data_ptr(), free_count.data_ptr(), free_blocks.numel(), int(page_size), T, cu_seqlens.data_ptr(),
-         seq_lens.data_ptr(), positions.data_ptr(), slots.data_ptr(), free_count_out.data_ptr())
+    blocks = free_blocks.numel()
+    _run("fa_kv_reserve", stream, _ints("ctx_lens", ctx_lens, R), _ints("new_lens", new_lens, R), R, table, stride, width,
+         _ints("free_blocks", free_blocks, blocks), _ints("free_count", free_count, 1), blocks, int(page_size), T,
+         _ints("cu_seqlens", cu_seqlens, R + 1), _ints("seq_lens", seq_lens, R), _ints("positions", positions, T),
+         _ints("slots", slots, T, _Types.i64), _ints("free_count_out", free_count_out, 1))
     return cu_seqlens, seq_lens, positions, slots, free_count_out
 
 
@@ -235,23 +256,26 @@ def fa_kv_release(lens, done, block_table, free_blocks, free_count, *, page_size
                   stream=None):
     """Gives the blocks of every request with done[r] != 0 back to the free stack (fa_kv_release);
     returns (lens_out [R], free_count_out [1]).  lens_out may be lens, free_count_out free_count."""
-    import torch
-    R = lens.shape[0]
-    _ints("lens", lens, (R,))
-    _ints("done", done, (R,))
+    if not _Types.ready:
+        _init()
+    R = lens.numel()
+    if lens_out is None:
+        lens_out = _empty((R,), _Types.i32, lens.device, stream)
+    if free_count_out is None:
+        free_count_out = _empty((1,), _Types.i32, lens.device, stream)
+    lens_p, done_p = _ints("lens", lens, R), _ints("done", done, R)
     table, stride, width = _table(block_table, R)
-    _ints("free_blocks", free_blocks, (free_blocks.numel(),))
-    _ints("free_count", free_count, (1,))
-    dev = lens.device
-    lens_out = _empty((R,), torch.int32, dev, stream) if lens_out is None else _ints("lens_out", lens_out, (R,))
-    free_count_out = _empty((1,), torch.int32, dev, stream) if free_count_out is None else _ints("free_count_out", free_count_out, (1,))
-    _run("fa_kv_release", stream, lens.data_ptr(), done.data_ptr(), R, table.data_ptr(), stride, width, free_blocks.data_ptr(),
-         free_count.data_ptr(), free_blocks.numel(), int(page_size), lens_out.data_ptr(), free_count_out.data_ptr())
+    blocks = free_blocks.numel()
+    _run("fa_kv_release", stream, lens_p, done_p, R, table, stride, width, _ints("free_blocks", free_blocks, blocks),
+         _ints("free_count", free_count, 1), blocks, int(page_size), _ints("lens_out", lens_out, R),
+         _ints("free_count_out", free_count_out, 1))
     return lens_out, free_count_out
 
 
 def paged_workspace_bytes(Hq: int, Hkv: int, d: int) -> int:
-    return int(_core().lib().fa_paged_workspace_bytes(int(Hq), int(Hkv), int(d)))
+    if not _Types.ready:
+        _init()
+    return int(_Types.fa.lib().fa_paged_workspace_bytes(int(Hq), int(Hkv), int(d)))
 
 
 def fa_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, *, max_new: int, causal: bool = True,
@@ -262,37 +286,38 @@ def fa_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, *, max_
     keys (the new tokens' own among them) in the blocks block_table[r] of the caches, logically
     [blocks, slots, Hkv, d].  Returns (out [T, Hq, d], lse [Hq, T] fp32 or None); rows of no request are
     left as they are in `out` and `lse` (undefined in buffers made here)."""
-    import torch
     f16 = _half(q)
-    qp, qs = _rows("q", q, q.dtype)
-    T, Hq, d = q.shape
+    dtype = q.dtype
+    qp, qs = _rows("q", q, dtype)
+    shape = q.shape
+    T, Hq, d = shape
     c = _cache(k_cache, v_cache)
-    if k_cache.dtype != q.dtype or c.d != d:
-        raise ValueError(f"shape mismatch q{tuple(q.shape)} {q.dtype} cache{tuple(k_cache.shape)} {k_cache.dtype}")
-    R = seq_lens.shape[0]
-    _ints("seq_lens", seq_lens, (R,))
-    _ints("cu_seqlens", cu_seqlens, (R + 1,))
+    if k_cache.dtype is not dtype or c.d != d:
+        raise ValueError(f"shape mismatch q{tuple(shape)} {dtype} cache{tuple(k_cache.shape)} {k_cache.dtype}")
+    R = seq_lens.numel()
     table, stride, width = _table(block_table, R)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
     if out is None:
-        out = _empty((T, Hq, d), q.dtype, q.device, stream)
-    elif out.dtype != q.dtype or tuple(out.shape) != (T, Hq, d) or not out.is_contiguous():
-        raise ValueError(f"out must be contiguous {q.dtype} {(T, Hq, d)}, got {out.dtype} {tuple(out.shape)}")
+        out = _empty(shape, dtype, q.device, stream)
+    elif out.dtype is not dtype or out.shape != shape or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous {dtype} {tuple(shape)}, got {out.dtype} {tuple(out.shape)}")
+    lse_p = None
     if not return_lse:
         lse = None
-    elif lse is None:
-        lse = _empty((Hq, T), torch.float32, q.device, stream)
-    elif lse.dtype != torch.float32 or tuple(lse.shape) != (Hq, T) or not lse.is_contiguous():
-        raise ValueError(f"lse must be contiguous fp32 {(Hq, T)}, got {lse.dtype} {tuple(lse.shape)}")
-    if window is not None and int(window) < 1:
+    else:
+        if lse is None:
+            lse = _empty((Hq, T), _Types.f32, q.device, stream)
+        elif lse.dtype is not _Types.f32 or lse.shape != (Hq, T) or not lse.is_contiguous():
+            raise ValueError(f"lse must be contiguous fp32 {(Hq, T)}, got {lse.dtype} {tuple(lse.shape)}")
+        lse_p = lse.data_ptr()
+    if window is None:
+        window = 0
+    elif int(window) < 1:
         raise ValueError(f"window must be at least 1, got {window}")
     if workspace is None:
-        workspace = _empty((max(1, paged_workspace_bytes(Hq, c.Hkv, d)),), torch.uint8, q.device, stream)
-    _run("fa_paged_fwd" + f16, stream, qp, qs, ctypes.byref(c), table.data_ptr(), stride, width, cu_seqlens.data_ptr(),
-         seq_lens.data_ptr(), R, T, Hq, int(max_new), float(scale), 1 if causal else 0, int(window) if window is not None else 0,
-         out.data_ptr(), lse.data_ptr() if lse is not None else None, workspace.data_ptr(),
-         workspace.numel() * workspace.element_size())
+        workspace = _empty((max(1, paged_workspace_bytes(Hq, c.Hkv, d)),), _Types.torch.uint8, q.device, stream)
+    _run("fa_paged_fwd" + f16, stream, qp, qs, ctypes.byref(c), table, stride, width, _ints("cu_seqlens", cu_seqlens, R + 1),
+         _ints("seq_lens", seq_lens, R), R, T, Hq, int(max_new), d ** -0.5 if scale is None else float(scale), 1 if causal else 0,
+         int(window), out.data_ptr(), lse_p, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out, lse
 
 
@@ -306,7 +331,9 @@ class PagedKV:
 
     def __init__(self, max_requests: int, num_blocks: int, page_size: int, Hkv: int, d: int, *, max_blocks: int | None = None,
                  dtype=None, device="cuda", layout: str = "nhd", tables: "PagedKV | None" = None):
-        import torch
+        if not _Types.ready:
+            _init()
+        torch = _Types.torch
         if layout not in ("nhd", "hnd"):
             raise ValueError(f"layout must be nhd or hnd, got {layout}")
         dtype = dtype or torch.bfloat16
@@ -332,7 +359,7 @@ class PagedKV:
         token are allowed: a captured step of fixed size).  Returns positions and slots."""
         if self.tables is not self:
             raise ValueError("reserve on the layer that holds the tables")
-        import torch
+        torch = _Types.torch
         if self.slots is None or self.slots.numel() != num_tokens:
             self.positions = _empty((num_tokens,), torch.int32, self.seq_lens.device, stream)
             self.slots = _empty((num_tokens,), torch.int64, self.seq_lens.device, stream)
