@@ -117,6 +117,9 @@ int encode_cache(CUtensorMap *mk, CUtensorMap *mv, const PagedParams &p, View kv
     return rc != FA_OK ? rc : encode_view(mv, p.v, d, kv.dims, kv.strides, cw, kv.box, f16 ? 1 : 0, line);
 }
 
+// What a unit of the few-rows kernel costs besides its steps (its Q, the first look-up, what it writes).
+constexpr int kRowOverhead = 2;
+
 // The kernel of few rows; fills what it adds to `p`.
 template <class C>
 int launch_rows_as(PagedParams &p, const View &kv, char *workspace, int ctas, int dev, cudaStream_t st) {
@@ -132,6 +135,7 @@ int launch_rows_as(PagedParams &p, const View &kv, char *workspace, int ctas, in
     p.plan.groups = p.Hq / p.pack;
     p.plan.tpb = C::ROWS / p.pack;
     p.plan.workers = ctas * C::WARPS;
+    p.plan.overhead = kRowOverhead;
     p.o_part = reinterpret_cast<float *>(workspace);
     p.lse_part = reinterpret_cast<float *>(workspace + part_o_bytes(p.plan.workers, C::ROWS, C::D));
     p.jobs = reinterpret_cast<MergeJob *>(workspace + part_bytes(p.plan.workers, C::ROWS, C::D));

@@ -141,6 +141,7 @@ struct PlanScan {
     static constexpr int NT = NT_;   // threads that take part = segments
     long long seg_start[NT + 1];
     long long warp_sum[NT / 32];
+    int warp_units[NT / 32];
     int seg_units[NT + 1];
 };
 
@@ -171,8 +172,9 @@ __device__ inline long long block_before(long long mine, long long *warp_sum, in
 // By all NT threads of the block.  Returns the total.
 template <int KS, int NT>
 __device__ inline long long plan_scan(const PlanParams &p, PlanScan<NT> &sh, int tid, bool say) {
-    const int seg = (p.R + NT - 1) / NT;
-    long long steps = 0, units = 0, total, total_units;
+    const int seg = (p.R + NT - 1) / NT, lane = tid % 32, warp = tid / 32;
+    long long steps = 0;
+    int units = 0;
     for (int r = tid * seg; r < min(p.R, (tid + 1) * seg); ++r) {
         const Request q = load_request(p, r, say);
         if (q.n > 0) {
@@ -180,11 +182,40 @@ __device__ inline long long plan_scan(const PlanParams &p, PlanScan<NT> &sh, int
             units += plan_units(p, q);
         }
     }
-    sh.seg_start[tid] = block_before<NT>(steps, sh.warp_sum, tid, total);
-    sh.seg_units[tid] = int(block_before<NT>(units, sh.warp_sum, tid, total_units));
+    long long upto = steps;
+    int units_upto = units;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+        const int z = __shfl_up_sync(0xffffffffu, units_upto, o);
+        if (lane >= o) {
+            upto += y;
+            units_upto += z;
+        }
+    }
+    if (lane == 31) {
+        sh.warp_sum[warp] = upto;
+        sh.warp_units[warp] = units_upto;
+    }
+    __syncthreads();
+    long long before = 0, total = 0;
+    int units_before = 0, total_units = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        const long long y = sh.warp_sum[w];
+        const int z = sh.warp_units[w];
+        if (w < warp) {
+            before += y;
+            units_before += z;
+        }
+        total += y;
+        total_units += z;
+    }
+    sh.seg_start[tid] = before + upto - steps;
+    sh.seg_units[tid] = units_before + units_upto - units;
     if (tid == 0) {
         sh.seg_start[NT] = total;
-        sh.seg_units[NT] = int(total_units);
+        sh.seg_units[NT] = total_units;
     }
     __syncthreads();
     return total;
@@ -223,6 +254,7 @@ template <int KS>
 FA_PLAN int find_block(const PlanParams &p, const Request &q, long long x, long long &before) {
     const int nb = plan_blocks(p, q);
     before = 0;
+    if (nb == 1) return 0;
 #ifdef __CUDA_ARCH__
     const int lane = int(threadIdx.x) % 32;
     for (int b0 = 0; b0 < nb; b0 += 32) {
@@ -257,6 +289,43 @@ FA_PLAN int find_block(const PlanParams &p, const Request &q, long long x, long 
 #endif
 }
 
+// A request on the line: its first step, and the steps of one head group.
+struct Place {
+    int r;
+    Request q;
+    long long at, group;
+};
+
+// The request that step x lies in, which is one of segment `lo`'s.
+template <int KS>
+FA_PLAN Place find_request(const PlanParams &p, const long long *steps_before, int lo, int seg, long long x) {
+    Place f{};
+    f.at = steps_before[lo];
+    for (f.r = lo * seg; f.r < p.R; ++f.r) {
+        f.q = load_request(p, f.r);
+        if (f.q.n == 0) continue;
+        f.group = plan_steps<KS>(p, f.q, plan_blocks(p, f.q));
+        if (x < f.at + f.group * p.groups) break;
+        f.at += f.group * p.groups;
+    }
+    return f;
+}
+
+// The unit of that request that step x lies in; by all threads of a warp.
+template <int KS>
+FA_PLAN Unit find_unit(const PlanParams &p, const Place &f, long long x) {
+    Unit u{};
+    u.r = f.r;
+    u.q = f.q;
+    u.g = int(div_pos(x - f.at, f.group));
+    const long long at = f.at + u.g * f.group;
+    long long before;
+    u.b = find_block<KS>(p, u.q, x - at, before);
+    u.begin = at + before;
+    plan_range<KS>(p, u.q, u.b, u.js, u.je);
+    return u;
+}
+
 // The unit that step x (0 <= x < total) lies in; by all threads of a warp.  `steps_before` are the
 // steps before each of `segments` segments of `seg` requests.
 template <int KS>
@@ -267,22 +336,7 @@ FA_PLAN Unit plan_find(const PlanParams &p, const long long *steps_before, int s
         if (steps_before[mid] <= x) lo = mid;
         else hi = mid;
     }
-    Unit u{};
-    long long at = steps_before[lo], group = 0;
-    for (u.r = lo * seg; u.r < p.R; ++u.r) {
-        u.q = load_request(p, u.r);
-        if (u.q.n == 0) continue;
-        group = plan_steps<KS>(p, u.q, plan_blocks(p, u.q));
-        if (x < at + group * p.groups) break;
-        at += group * p.groups;
-    }
-    u.g = int(div_pos(x - at, group));
-    at += u.g * group;
-    long long before;
-    u.b = find_block<KS>(p, u.q, x - at, before);
-    u.begin = at + before;
-    plan_range<KS>(p, u.q, u.b, u.js, u.je);
-    return u;
+    return find_unit<KS>(p, find_request<KS>(p, steps_before, lo, seg, x), x);
 }
 
 // Unit number k (0 <= k < units) of the line, without its place on it (begin = 0); `units_before` are

@@ -49,6 +49,7 @@ struct PagedParams {
 
 constexpr int kRowRows = 16;       // rows a unit at most
 constexpr int kMaxPagedCtas = 192;
+constexpr int kCachedRequests = 512;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Keys a step, warps a CTA, rows a unit (8 or 16), pages by TMA, and the ring's depth.  A step costs a
@@ -166,18 +167,23 @@ struct Found {
 // The loading side of a worker: a step ahead of the copies, each lane knows where one key lies.
 template <class C>
 struct KeyStream {
-    Unit u;
-    int j, left;               // next step of the unit, steps left
+    Walk walk;
+    Piece piece;
+    int j;                     // the piece's next step
+    bool any;                  // there is one
     int key, page, slot;       // this lane's key of step j (or its box's first), its page and slot
     int span;                  // keys of which that is the first
     int lo, hi;                // keys that the unit sees
     const int *table;
     int head;                  // KV head
 
-    __device__ __forceinline__ void enter(const PagedParams &p) {
-        unit_keys(p.plan, u, lo, hi);
-        table = p.table + u.r * p.table_stride;
-        head = u.g * p.pack / p.n_rep;
+    __device__ __forceinline__ void enter(const PagedParams &p, const PlanParams &plan) {
+        any = walk_next<C::KEYS>(plan, walk, piece);
+        if (!any) return;
+        j = piece.js;
+        unit_keys(plan, piece.u, lo, hi);
+        table = p.table + piece.u.r * p.table_stride;
+        head = piece.u.g * p.pack / p.n_rep;
         span = C::TMA ? p.run : 1;
         key = j * C::KEYS + int(threadIdx.x) * span % C::KEYS;
         page = key / p.page;
@@ -187,17 +193,17 @@ struct KeyStream {
     // it may have to come from L2.
     __device__ __forceinline__ Found find() const {
         Found f;
-        f.seen = left > 0 && key <= hi && key + span > lo;
+        f.seen = any && key <= hi && key + span > lo;
         f.id = f.seen ? __ldg(table + page) : 0;
         f.slot = slot;
-        f.r = u.r;
+        f.r = piece.u.r;
         f.head = head;
-        f.any = left > 0;
+        f.any = any;
         return f;
     }
-    __device__ __forceinline__ void step(const PagedParams &p) {
-        if (--left <= 0) return;
-        if (++j < u.je) {
+    __device__ __forceinline__ void step(const PagedParams &p, const PlanParams &plan) {
+        if (!any) return;
+        if (++j < piece.je) {
             key += C::KEYS;
             slot += C::KEYS;
             if (slot >= p.page) {
@@ -209,9 +215,7 @@ struct KeyStream {
                 }
             }
         } else {
-            plan_next<C::KEYS>(p.plan, u);
-            j = u.js;
-            enter(p);
+            enter(p, plan);
         }
     }
 };
@@ -224,30 +228,61 @@ fa_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ PlanScan<C::THREADS> scan;
     __shared__ uint64_t landed[C::WARPS][C::STAGES];   // a step's rows are in their slot
+    __shared__ Place places[C::WARPS];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge may be set up meanwhile
-    const int lane = int(threadIdx.x) % 32, warp = int(threadIdx.x) / 32;
-    const long long total = plan_scan<C::KEYS>(p.plan, scan, int(threadIdx.x), blockIdx.x == 0 && p.say != 0);
-    // Neighbouring workers are on different SMs, so that few of them spread out.
-    const int worker = warp * int(gridDim.x) + int(blockIdx.x);
-    // A call too small for all: a unit of U steps in pieces of s costs s steps and then the merge of U / s
-    // pieces, eight loads of them at a time; with a step and such a round about equally long, s^2 = U / 8.
+    const int tid = int(threadIdx.x), lane = tid % 32, warp = tid / 32;
+    if (C::TMA && tid == 0) {
+        sm100::prefetch_tensormap(&tm_k);
+        sm100::prefetch_tensormap(&tm_v);
+    }
+    // Lengths in shared memory, where they fit: a worker that goes from one request to the next asks for
+    // them in the middle of its stream.
+    __shared__ int lengths[2 * kCachedRequests + 1];
+    PlanParams plan = p.plan;
+    if (plan.R <= kCachedRequests) {
+        for (int i = tid; i <= plan.R; i += C::THREADS) {
+            lengths[i] = p.plan.cu[i];
+            if (i < plan.R) lengths[kCachedRequests + 1 + i] = p.plan.lens[i];
+        }
+        plan.cu = lengths;
+        plan.lens = lengths + kCachedRequests + 1;
+        __syncthreads();
+    }
+    const long long total = plan_scan<C::KEYS>(plan, scan, tid, blockIdx.x == 0 && p.say != 0);
+    // A call too small for all workers: a unit of U steps in pieces of s costs s steps and then the merge of
+    // U / s pieces, eight loads of them at a time; with a step and such a round about equally long, s^2 = U / 8.
     const float mean = float(total) / float(max(1, scan.seg_units[C::THREADS]));
     const long long least = max(2LL, (long long)sqrtf(mean * 0.125f));
-    const int workers = int(max(1LL, min((long long)p.plan.workers, total / least)));
-    const long long x0 = worker < workers ? range_start(total, workers, worker) : total;
-    const long long x1 = worker < workers ? range_start(total, workers, worker + 1) : total;
+    const int workers = int(max(1LL, min((long long)p.plan.workers, div_pos(total, least))));
+    const long long share = div_pos(total, workers), more = total - share * workers;   // as range_start
+    // Neighbouring workers are on different SMs, so that few of them spread out.
+    auto worker_of = [&](int w) { return w * int(gridDim.x) + int(blockIdx.x); };
+    auto start_of = [&](int i) { return i < workers ? i * share + min((long long)i, more) : total; };
+    {   // the thread whose requests hold a worker's first step finds it
+        const long long from = scan.seg_start[tid], to = scan.seg_start[tid + 1];
+#pragma unroll 1
+        for (int w = 0; w < C::WARPS; ++w) {
+            const long long x = start_of(worker_of(w));
+            if (x >= from && x < to)
+                places[w] = find_request<C::KEYS>(plan, scan.seg_start, tid, (plan.R + C::THREADS - 1) / C::THREADS, x);
+        }
+    }
+    __syncthreads();
+    const int worker = worker_of(warp);
+    const long long x0 = start_of(worker), x1 = start_of(worker + 1);
     if (x0 >= x1) {
         if (lane == 0) p.jobs[worker].parts = 0;
         return;
     }
 
+    Walk walk{};                // the computing side's
+    walk.u = find_unit<C::KEYS>(plan, places[warp], x0);
+    walk.o = x0 - walk.u.begin;
+    walk.left = x1 - x0;
+    walk.first = true;
     KeyStream<C> load;
-    load.u = plan_find<C::KEYS>(p.plan, scan.seg_start, C::THREADS, (p.plan.R + C::THREADS - 1) / C::THREADS, x0);
-    load.j = load.u.js + int(x0 - load.u.begin);
-    load.left = int(min(x1 - x0, 0x7fffffffLL));
-    Unit u = load.u;            // the computing side: unit, step, steps left
-    int j = load.j, left = load.left;
-    load.enter(p);
+    load.walk = walk;
+    load.enter(p, plan);
 
     const uint32_t ring0 = C::TMA ? (sm100::smem_u32(ring) + 1023u) & ~1023u : sm100::smem_u32(ring);
     const uint32_t base = ring0 + uint32_t(warp * C::STAGES * C::STAGE);
@@ -306,7 +341,7 @@ fa_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     uint32_t parity = 0;
     // Sends the step that was looked up last to the next ring slot, and looks up the one after it.
     auto send = [&]() {
-        load.step(p);
+        load.step(p, plan);
         const Found next = load.find();
         send_rows(found, put);
         put = put + 1 == C::STAGES ? 0 : put + 1;
@@ -316,7 +351,7 @@ fa_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     for (int s = 0; s < C::STAGES - 1; ++s) send();
     if (lane == 0) {
         MergeJob job{};
-        if (worker > 0) job = merge_job(p.plan, u, worker, workers, [&](int w) { return range_start(total, workers, w); });
+        if (worker > 0) job = merge_job(plan, walk.u, worker, workers, start_of);
         p.jobs[worker] = job;
     }
 
@@ -325,10 +360,6 @@ fa_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     float o[NR][D / 16][4];           // O^T: d lane / 4 (+ 8), columns 2 (lane % 4), + 1
     float m[NR][2], l[NR][2];         // of those columns
     int lo[NR][2], hi[NR][2];
-    int clear_lo = 0, clear_hi = -1;  // keys that every row of the unit sees
-    int tokens = 0, unit_lo = 0, unit_hi = 0;
-    int j0 = j;                       // first step of the piece of this unit
-    bool fresh = true;
     const int t2 = (lane & 3) * 2, g = lane >> 2;
     // ldmatrix rows and units: K (matrices: keys 0-7 | 8-15 | 0-7 | 8-15, units 0 | 0 | 1 | 1) and V,
     // transposed (keys 0-7 | 0-7 | 8-15 | 8-15, units 0 | 1 | 0 | 1)
@@ -347,143 +378,148 @@ fa_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     };
     const Lines k_at((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4), v_at((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
 
+    Piece piece;
 #pragma unroll 1
-    while (left > 0) {
-        if (fresh) {
-            tokens = min(p.plan.tpb, u.q.n - u.b * p.plan.tpb);
+    while (walk_next<C::KEYS>(plan, walk, piece)) {
+        const Unit &u = piece.u;
+        const int tokens = min(plan.tpb, u.q.n - u.b * plan.tpb);
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int i = (8 * r + t2 + c) / p.pack;
-                    token_keys(p.plan, u.q, u.b * p.plan.tpb + i, lo[r][c], hi[r][c]);
-                    m[r][c] = -INFINITY;
-                    l[r][c] = 0.f;
-                }
-                const int row = 8 * r + g, i = row / p.pack;
-                const uint16_t *src = p.q + (long long)(u.q.q0 + u.b * p.plan.tpb + i) * p.q_stride +
-                                      (long long)(u.g * p.pack + row - i * p.pack) * D + t2;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    qf[r][kk][0] = i < tokens ? *reinterpret_cast<const uint32_t *>(src + 16 * kk) : 0u;
-                    qf[r][kk][1] = i < tokens ? *reinterpret_cast<const uint32_t *>(src + 16 * kk + 8) : 0u;
-                }
-#pragma unroll
-                for (int n = 0; n < D / 16; ++n) o[r][n][0] = o[r][n][1] = o[r][n][2] = o[r][n][3] = 0.f;
-            }
-            unit_keys(p.plan, u, unit_lo, unit_hi);
-            int any_hi, any_lo;   // the first token sees the least, the last one loses the most
-            token_keys(p.plan, u.q, u.b * p.plan.tpb, any_lo, clear_hi);
-            token_keys(p.plan, u.q, u.b * p.plan.tpb + tokens - 1, clear_lo, any_hi);
-            fresh = false;
-        }
-        if (!__all_sync(0xffffffffu, wait_rows(bars + 8u * get, parity, p.plan.status))) {
-            // gives up: the copies still on their way land before the warp ends (the last ones of each slot)
-            for (int s = 0; s < C::STAGES; ++s)
-                if (s != get) wait_rows(bars + 8u * s, s > get ? parity : parity ^ 1u, p.plan.status);
-            return;
-        }
-        send();   // into the slot that the step before this one used
-        const uint32_t tile = base + uint32_t(get * C::STAGE);
-        if (++get == C::STAGES) {
-            get = 0;
-            parity ^= 1u;
-        }
-        const int first = j * C::KEYS;
-        if (C::TMA && (first < unit_lo || first + C::KEYS - 1 > unit_hi)) {   // V's rows outside the unit's keys
-            const int row = lane % C::KEYS, part = lane / C::KEYS, parts = 32 / C::KEYS;
-            if (first + row < unit_lo || first + row > unit_hi)
-#pragma unroll 1
-                for (int i = part * 16; i < C::NCH * C::RB; i += parts * 16)
-                    sm100::st_shared_v4(tile + uint32_t(C::TILE + i / C::RB * C::CHUNK + row * C::RB + i % C::RB), 0u, 0u, 0u, 0u);
-            sm100::fence_proxy_async_smem();   // before the slot's next copies
-            __syncwarp();
-        }
-        // Rows that are not there need no mask either: their Q is zero and nothing of theirs is written.
-        const bool masked = first < clear_lo || first + C::KEYS - 1 > clear_hi;
-
-        // All of K's fragments are asked for before the first product, and all of V's before the softmax,
-        // whose chain then covers their way from shared memory.
-        float s[C::KEYS / 16][NR][4] = {};
-        uint32_t f[D / 16][C::KEYS / 16][4];
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-            for (int k = 0; k < C::KEYS / 16; ++k) ldmatrix4(f[kk][k], tile + k_at(kk, k));
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-            for (int k = 0; k < C::KEYS / 16; ++k)
-#pragma unroll
-                for (int r = 0; r < NR; ++r) mma16816<C::F16>(s[k][r], f[kk][k], qf[r][kk][0], qf[r][kk][1]);
-#pragma unroll
-        for (int n = 0; n < D / 16; ++n)
-#pragma unroll
-            for (int k = 0; k < C::KEYS / 16; ++k) ldmatrix4_trans(f[n][k], tile + uint32_t(C::TILE) + v_at(n, k));
-        if (masked) {
-#pragma unroll
-            for (int k = 0; k < C::KEYS / 16; ++k)
-#pragma unroll
-                for (int r = 0; r < NR; ++r)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = first + 16 * k + g + 8 * (e >> 1), c = e & 1;
-                        if (key < lo[r][c] || key > hi[r][c]) s[k][r][e] = -INFINITY;
-                    }
-        }
-        bool grew = false;
-        float alpha[NR][2], ref[NR][2];
-#pragma unroll
-        for (int r = 0; r < NR; ++r)
+        for (int r = 0; r < NR; ++r) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                float mx = -INFINITY;
-#pragma unroll
-                for (int k = 0; k < C::KEYS / 16; ++k) mx = fmaxf(mx, fmaxf(s[k][r][c], s[k][r][2 + c]));
-#pragma unroll
-                for (int x = 4; x < 32; x *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-                const float now = fmaxf(m[r][c], mx * p.scale_log2);
-                ref[r][c] = now == -INFINITY ? 0.f : now;
-                alpha[r][c] = sm100::ex2_approx(m[r][c] - ref[r][c]);   // (before the first key: 0, times sums of 0)
-                grew |= now != m[r][c];
-                m[r][c] = now;
+                const int i = (8 * r + t2 + c) / p.pack;
+                token_keys(plan, u.q, u.b * plan.tpb + i, lo[r][c], hi[r][c]);
+                m[r][c] = -INFINITY;
+                l[r][c] = 0.f;
             }
-        if (__any_sync(0xffffffffu, grew)) {
+            const int row = 8 * r + g, i = row / p.pack;
+            const uint16_t *src = p.q + (long long)(u.q.q0 + u.b * plan.tpb + i) * p.q_stride +
+                                  (long long)(u.g * p.pack + row - i * p.pack) * D + t2;
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
-                l[r][0] *= alpha[r][0];
-                l[r][1] *= alpha[r][1];
-#pragma unroll
-                for (int n = 0; n < D / 16; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[r][n][e] *= alpha[r][e & 1];
+            for (int kk = 0; kk < D / 16; ++kk) {
+                qf[r][kk][0] = i < tokens ? *reinterpret_cast<const uint32_t *>(src + 16 * kk) : 0u;
+                qf[r][kk][1] = i < tokens ? *reinterpret_cast<const uint32_t *>(src + 16 * kk + 8) : 0u;
             }
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n) o[r][n][0] = o[r][n][1] = o[r][n][2] = o[r][n][3] = 0.f;
         }
-        uint32_t pf[C::KEYS / 16][NR][2];   // P^T: keys 2 (lane % 4) (+ 8), columns lane / 4
-#pragma unroll
-        for (int k = 0; k < C::KEYS / 16; ++k)
-#pragma unroll
-            for (int r = 0; r < NR; ++r) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[k][r][e] = sm100::ex2_approx(fmaf(s[k][r][e], p.scale_log2, -ref[r][e & 1]));
-                    l[r][e & 1] += s[k][r][e];
-                }
-                pf[k][r][0] = movmatrix(sm100::pack_x2<C::F16>(s[k][r][0], s[k][r][1]));
-                pf[k][r][1] = movmatrix(sm100::pack_x2<C::F16>(s[k][r][2], s[k][r][3]));
+        int unit_lo, unit_hi, clear_lo, clear_hi, any_hi, any_lo;
+        unit_keys(plan, u, unit_lo, unit_hi);
+        // keys that every row of the unit sees: the first token sees the least, the last one loses the most
+        token_keys(plan, u.q, u.b * plan.tpb, any_lo, clear_hi);
+        token_keys(plan, u.q, u.b * plan.tpb + tokens - 1, clear_lo, any_hi);
+
+#pragma unroll 1
+        for (int j = piece.js; j < piece.je; ++j) {
+            if (!__all_sync(0xffffffffu, wait_rows(bars + 8u * get, parity, p.plan.status))) {
+                // gives up: the copies still on their way land before the warp ends (the last ones of each slot)
+                for (int s = 0; s < C::STAGES; ++s)
+                    if (s != get) wait_rows(bars + 8u * s, s > get ? parity : parity ^ 1u, p.plan.status);
+                return;
             }
+            send();   // into the slot that the step before this one used
+            const uint32_t tile = base + uint32_t(get * C::STAGE);
+            if (++get == C::STAGES) {
+                get = 0;
+                parity ^= 1u;
+            }
+            const int first = j * C::KEYS;
+            if (C::TMA && (first < unit_lo || first + C::KEYS - 1 > unit_hi)) {   // V's rows outside the unit's keys
+                const int row = lane % C::KEYS, part = lane / C::KEYS, parts = 32 / C::KEYS;
+                if (first + row < unit_lo || first + row > unit_hi)
+#pragma unroll 1
+                    for (int i = part * 16; i < C::NCH * C::RB; i += parts * 16)
+                        sm100::st_shared_v4(tile + uint32_t(C::TILE + i / C::RB * C::CHUNK + row * C::RB + i % C::RB), 0u, 0u, 0u, 0u);
+                sm100::fence_proxy_async_smem();   // before the slot's next copies
+                __syncwarp();
+            }
+            // Rows that are not there need no mask either: their Q is zero and nothing of theirs is written.
+            const bool masked = first < clear_lo || first + C::KEYS - 1 > clear_hi;
+
+            // All of K's fragments are asked for before the first product, and all of V's before the softmax,
+            // whose chain then covers their way from shared memory.
+            float s[C::KEYS / 16][NR][4] = {};
+            uint32_t f[D / 16][C::KEYS / 16][4];
 #pragma unroll
-        for (int k = 0; k < C::KEYS / 16; ++k)
+            for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                for (int k = 0; k < C::KEYS / 16; ++k) ldmatrix4(f[kk][k], tile + k_at(kk, k));
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                for (int k = 0; k < C::KEYS / 16; ++k)
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) mma16816<C::F16>(s[k][r], f[kk][k], qf[r][kk][0], qf[r][kk][1]);
 #pragma unroll
             for (int n = 0; n < D / 16; ++n)
 #pragma unroll
-                for (int r = 0; r < NR; ++r) mma16816<C::F16>(o[r][n], f[n][k], pf[k][r][0], pf[k][r][1]);
-        __syncwarp();   // the slot may be filled again
+                for (int k = 0; k < C::KEYS / 16; ++k) ldmatrix4_trans(f[n][k], tile + uint32_t(C::TILE) + v_at(n, k));
+            if (masked) {
+#pragma unroll
+                for (int k = 0; k < C::KEYS / 16; ++k)
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = first + 16 * k + g + 8 * (e >> 1), c = e & 1;
+                            if (key < lo[r][c] || key > hi[r][c]) s[k][r][e] = -INFINITY;
+                        }
+            }
+            bool grew = false;
+            float alpha[NR][2], ref[NR][2];
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < C::KEYS / 16; ++k) mx = fmaxf(mx, fmaxf(s[k][r][c], s[k][r][2 + c]));
+#pragma unroll
+                    for (int x = 4; x < 32; x *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+                    const float now = fmaxf(m[r][c], mx * p.scale_log2);
+                    ref[r][c] = now == -INFINITY ? 0.f : now;
+                    alpha[r][c] = sm100::ex2_approx(m[r][c] - ref[r][c]);   // (before the first key: 0, times sums of 0)
+                    grew |= now != m[r][c];
+                    m[r][c] = now;
+                }
+            if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    l[r][0] *= alpha[r][0];
+                    l[r][1] *= alpha[r][1];
+#pragma unroll
+                    for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[r][n][e] *= alpha[r][e & 1];
+                }
+            }
+            uint32_t pf[C::KEYS / 16][NR][2];   // P^T: keys 2 (lane % 4) (+ 8), columns lane / 4
+#pragma unroll
+            for (int k = 0; k < C::KEYS / 16; ++k)
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        s[k][r][e] = sm100::ex2_approx(fmaf(s[k][r][e], p.scale_log2, -ref[r][e & 1]));
+                        l[r][e & 1] += s[k][r][e];
+                    }
+                    pf[k][r][0] = movmatrix(sm100::pack_x2<C::F16>(s[k][r][0], s[k][r][1]));
+                    pf[k][r][1] = movmatrix(sm100::pack_x2<C::F16>(s[k][r][2], s[k][r][3]));
+                }
+#pragma unroll
+            for (int k = 0; k < C::KEYS / 16; ++k)
+#pragma unroll
+                for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) mma16816<C::F16>(o[r][n], f[n][k], pf[k][r][0], pf[k][r][1]);
+            __syncwarp();   // the slot may be filled again
 
-        ++j;
-        if (--left == 0 || j == u.je) {   // the end of this unit's piece
-            const bool whole = j0 == u.js && j == u.je;
-            const int slot = 2 * worker + (j0 - u.js + u.begin == x0 ? 0 : 1);
+        }
+
+        // the piece is done
+        {
+            const bool whole = piece.js == u.js && piece.je == u.je;
+            const int slot = 2 * worker + (piece.first ? 0 : 1);
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
                 float inv[2], lse[2];
@@ -497,7 +533,7 @@ fa_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 }
                 if (whole) {   // transposed back: row g, d 2 (lane % 4), + 1
                     const int row = 8 * r + g, i = row / p.pack;
-                    const long long at_row = u.q.q0 + u.b * p.plan.tpb + i;
+                    const long long at_row = u.q.q0 + u.b * plan.tpb + i;
                     uint16_t *dst = p.out + (at_row * p.Hq + u.g * p.pack + row - i * p.pack) * D + t2;
 #pragma unroll
                     for (int n = 0; n < D / 16; ++n)
@@ -513,7 +549,7 @@ fa_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                     if (i >= tokens) continue;
                     if (whole) {
                         if (p.lse != nullptr && g == 0)
-                            p.lse[(long long)(u.g * p.pack + row - i * p.pack) * p.plan.T + u.q.q0 + u.b * p.plan.tpb + i] = lse[c];
+                            p.lse[(long long)(u.g * p.pack + row - i * p.pack) * p.plan.T + u.q.q0 + u.b * plan.tpb + i] = lse[c];
                     } else {
                         const long long at_row = (long long)slot * C::ROWS + row;
                         float *dst = p.o_part + at_row * D + g;
@@ -525,11 +561,6 @@ fa_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                         if (g == 0) p.lse_part[at_row] = lse[c];
                     }
                 }
-            }
-            fresh = true;
-            if (left > 0) {
-                plan_next<C::KEYS>(p.plan, u);
-                j0 = j = u.js;
             }
         }
     }
@@ -611,16 +642,15 @@ __device__ __forceinline__ void merge_unit(const PagedParams &p, const MergeJob 
                 share[warp][PER * VEC * 32 + 1] = sum;
             }
             __syncthreads();
-            if (helper != 0) return;
             float all = m;
-            for (int h = 1; h < helpers; ++h) all = fmaxf(all, share[warp + h * side_by_side][PER * VEC * 32]);
+            for (int h = 1; helper == 0 && h < helpers; ++h) all = fmaxf(all, share[warp + h * side_by_side][PER * VEC * 32]);
             const float keep = all == -INFINITY ? 0.f : __expf(m - all);
             sum *= keep;
 #pragma unroll
             for (int e = 0; e < PER; ++e)
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) acc[e][v] *= keep;
-            for (int h = 1; h < helpers; ++h) {
+            for (int h = 1; helper == 0 && h < helpers; ++h) {
                 const float *other = share[warp + h * side_by_side];
                 const float wt = all == -INFINITY ? 0.f : __expf(other[PER * VEC * 32] - all);
                 sum = fmaf(wt, other[PER * VEC * 32 + 1], sum);
@@ -631,7 +661,7 @@ __device__ __forceinline__ void merge_unit(const PagedParams &p, const MergeJob 
             }
             m = all;
         }
-        if (!real) continue;
+        if (!real || helper != 0) continue;
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
         const long long at = job.row0 + token;
 #pragma unroll

@@ -12,7 +12,9 @@
 //
 // Bound by memory: every value is read once and written once, 16 bytes a thread at a time.  A CTA
 // takes TOK tokens and all heads; a thread keeps its (head, 16 values) over the TOK tokens, so the
-// index arithmetic is done once and 2 TOK loads are in flight together.
+// index arithmetic is done once and 2 TOK loads are in flight together.  The block has as many threads
+// as there are such units (or an even share of them), and the first loads are on their way while the
+// angles are computed.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -29,7 +31,8 @@ namespace {
 
 using namespace fa_host;
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 512;   // at most
+constexpr int kRopeTokens = 4;      // tokens a CTA, where there are many
 constexpr int kMaxPairs = 128;   // rot_dim <= 256
 constexpr int kMaxAxes = 4;
 
@@ -99,6 +102,7 @@ __device__ __forceinline__ void stage_tokens(const RopeParams &p, long long t0, 
         }
         row[tid] = at;
     }
+#pragma unroll 1
     for (int w = tid; w < TOK * half; w += int(blockDim.x)) {
         const int tok = w / half, i = w - tok * half;
         const long long t = t0 + tok;
@@ -149,29 +153,34 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const __grid_cons
     extern __shared__ float2 angles[];
     __shared__ long long row[TOK];
     const long long t0 = (long long)blockIdx.x * TOK;
-    stage_tokens<TOK>(p, t0, row, angles);
     const int half = p.rot / 2, per_head = p.d / 16;
-    const int heads = p.Hq + p.Hkv + (p.v_cache != nullptr ? p.Hkv : 0);
-    for (int u = int(threadIdx.x); u < heads * per_head; u += kRopeThreads) {
+    const int heads = p.Hq + p.Hkv + (p.v_cache != nullptr ? p.Hkv : 0), units = heads * per_head;
+    const int here = int(min((long long)TOK, p.T - t0));   // tokens of this CTA
+    bool staged = false;
+    for (int u = int(threadIdx.x); u < units || !staged; u += int(blockDim.x)) {
         const int h = u / per_head, i = u - h * per_head;
-        const Lane l = head_lane(p, h, t0);
+        Lane l{};
+        if (u < units) l = head_lane(p, h, t0);
         const bool turn = l.turn && 16 * i < p.rot;
         const bool split = turn && p.interleaved == 0;
         const int e0 = split ? 8 * i : 16 * i, e1 = split ? half + 8 * i : 16 * i + 8;
         const int a0 = 8 * i;   // first pair of the unit
         uint4 x[TOK][2];
-        bool there[TOK];
 #pragma unroll
         for (int tok = 0; tok < TOK; ++tok) {
-            there[tok] = row[tok] >= 0;
-            if (there[tok]) {
+            if (u < units && tok < here) {
                 x[tok][0] = __ldcs(reinterpret_cast<const uint4 *>(l.src + tok * l.src_stride + e0));
                 x[tok][1] = __ldcs(reinterpret_cast<const uint4 *>(l.src + tok * l.src_stride + e1));
             }
         }
+        if (!staged) {   // (every thread comes here once: in its first round, with a unit or without)
+            stage_tokens<TOK>(p, t0, row, angles);
+            staged = true;
+        }
+        if (u >= units) break;
 #pragma unroll
         for (int tok = 0; tok < TOK; ++tok) {
-            if (!there[tok]) continue;
+            if (row[tok] < 0) continue;
             uint32_t a[4] = {x[tok][0].x, x[tok][0].y, x[tok][0].z, x[tok][0].w};
             uint32_t b[4] = {x[tok][1].x, x[tok][1].y, x[tok][1].z, x[tok][1].w};
             if (turn) {
@@ -212,7 +221,7 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_any_kernel(const __grid_
     const int half = p.rot / 2;
     const int heads = p.Hq + p.Hkv + (p.v_cache != nullptr ? p.Hkv : 0);
     const int per_head = half + (p.d - p.rot);   // pairs, then single values
-    for (int u = int(threadIdx.x); u < heads * per_head; u += kRopeThreads) {
+    for (int u = int(threadIdx.x); u < heads * per_head; u += int(blockDim.x)) {
         const int h = u / per_head, i = u - h * per_head;
         const Lane l = head_lane(p, h, t0);
         uint16_t *dst = l.dst + (l.cache ? row[0] : 0);
@@ -238,12 +247,16 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_any_kernel(const __grid_
 template <bool F16>
 int launch(const RopeParams &p, bool vec, int num_sms, cudaStream_t st) {
     const size_t per_token = size_t(p.rot / 2) * sizeof(float2);
+    const int heads = p.Hq + p.Hkv + (p.v_cache != nullptr ? p.Hkv : 0);
+    const int units = vec ? heads * (p.d / 16) : heads * (p.d - p.rot / 2), rounds = (units + kRopeThreads - 1) / kRopeThreads;
+    const unsigned threads = unsigned(((units + rounds - 1) / rounds + 31) / 32 * 32);
     if (!vec) {
-        fa_rope_any_kernel<F16><<<unsigned(p.T), kRopeThreads, per_token, st>>>(p);
+        fa_rope_any_kernel<F16><<<unsigned(p.T), threads, per_token, st>>>(p);
     } else if (p.T <= 4 * num_sms) {
-        fa_rope_kernel<F16, 1><<<unsigned(p.T), kRopeThreads, per_token, st>>>(p);
+        fa_rope_kernel<F16, 1><<<unsigned(p.T), threads, per_token, st>>>(p);
     } else {
-        fa_rope_kernel<F16, 4><<<unsigned((p.T + 3) / 4), kRopeThreads, 4 * per_token, st>>>(p);
+        constexpr int TOK = kRopeTokens;
+        fa_rope_kernel<F16, TOK><<<unsigned((p.T + TOK - 1) / TOK), threads, TOK * per_token, st>>>(p);
     }
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

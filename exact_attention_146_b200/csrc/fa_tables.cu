@@ -30,6 +30,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kTableThreads = 1024;
 constexpr int kMaxCluster = 8;
+constexpr int kBatch = 4;   // tokens or blocks a thread has in flight
 
 // Inclusive scan over the block of a pair of sums packed in 64 bits (low: tokens, high: blocks;
 // each below 2^31, so the halves never carry).  `warp_sums`: 32 words of shared memory.
@@ -152,20 +153,34 @@ __global__ void __launch_bounds__(kTableThreads) fa_kv_reserve_kernel(const __gr
             if (rank == 0 && r < p.R) p.cu[r] = s_cu[tid];
             __syncthreads();
             const int tok_end = tok_base + int(total & 0xffffffffu), blk_end = blk_base + int(total >> 32);
-            for (int t = tok_base + rank * nt + tid; t < tok_end; t += ranks * nt) {
-                const int i = holder(s_cu, n_here, t);
-                const int pos = s_ctx[i] + t - s_cu[i];
-                const int lb = pos / p.page;
-                const bool old = lb < s_held[i];
-                const int id = old ? p.table[(long long)(base + i) * p.table_stride + lb]
+            // kBatch tokens a thread at a time: their searches and loads overlap
+            const int step = ranks * nt;
+            for (int t0 = tok_base + rank * nt + tid; t0 < tok_end; t0 += kBatch * step) {
+                int id[kBatch], pos[kBatch], in_page[kBatch], at[kBatch];
+                bool old[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int t = min(t0 + k * step, tok_end - 1), i = holder(s_cu, n_here, t);
+                    pos[k] = s_ctx[i] + t - s_cu[i];
+                    const int lb = pos[k] / p.page;
+                    in_page[k] = pos[k] - lb * p.page;
+                    at[k] = base + i;
+                    old[k] = lb < s_held[i];
+                    id[k] = old[k] ? p.table[(long long)(base + i) * p.table_stride + lb]
                                    : p.free_blocks[count - 1 - (s_off[i] + lb - s_held[i])];
-                long long slot = (long long)id * p.page + (pos - lb * p.page);
-                if (id < 0 || id >= p.num_blocks) {
-                    report_range(p.status, old ? kSiteTableId : kSiteFreeId, base + i);
-                    slot = -1;
                 }
-                p.positions[t] = pos;
-                p.slots[t] = slot;
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int t = t0 + k * step;
+                    if (t >= tok_end) break;
+                    long long slot = (long long)id[k] * p.page + in_page[k];
+                    if (id[k] < 0 || id[k] >= p.num_blocks) {
+                        report_range(p.status, old[k] ? kSiteTableId : kSiteFreeId, at[k]);
+                        slot = -1;
+                    }
+                    p.positions[t] = pos[k];
+                    p.slots[t] = slot;
+                }
             }
             for (int b = blk_base + rank * nt + tid; b < blk_end; b += ranks * nt) {
                 const int i = holder(s_off, n_here, b);
@@ -241,11 +256,22 @@ __global__ void __launch_bounds__(kTableThreads) fa_kv_release_kernel(const __gr
             s_off[tid] = blk_base + int(upto) - held;
             __syncthreads();
             const int blk_end = blk_base + int(total);
-            for (int b = blk_base + rank * nt + tid; b < blk_end; b += ranks * nt) {
-                const int i = holder(s_off, n_here, b);
-                const int id = p.table[(long long)(base + i) * p.table_stride + (b - s_off[i])];
-                if (id < 0 || id >= p.num_blocks) report_range(p.status, kSiteTableId, base + i);
-                p.free_blocks[count + b] = id;
+            const int step = ranks * nt;
+            for (int b0 = blk_base + rank * nt + tid; b0 < blk_end; b0 += kBatch * step) {
+                int id[kBatch], at[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int b = min(b0 + k * step, blk_end - 1), i = holder(s_off, n_here, b);
+                    at[k] = base + i;
+                    id[k] = p.table[(long long)(base + i) * p.table_stride + (b - s_off[i])];
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int b = b0 + k * step;
+                    if (b >= blk_end) break;
+                    if (id[k] < 0 || id[k] >= p.num_blocks) report_range(p.status, kSiteTableId, at[k]);
+                    p.free_blocks[count + b] = id[k];
+                }
             }
             blk_base = blk_end;
             __syncthreads();

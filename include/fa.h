@@ -347,8 +347,8 @@ typedef struct fa_rope_spec {
  *   no output row may overlap an input row or another output row.
  * fa_rope_append: q as above (forward turn; q_out NULL with Hq = 0), and for each token t with
  *   slots[t] >= 0 the rotated k row and the v row go to slot slots[t] % page_size of block
- *   slots[t] / page_size of the cache.  Rows with a negative slot are left out: neither read
- *   nor written, q_out included.  A slot >= num_blocks * page_size is left out too and reported
+ *   slots[t] / page_size of the cache.  Rows with a negative slot are left out: nothing
+ *   of theirs is written, q_out included.  A slot >= num_blocks * page_size is left out too and reported
  *   (FA_ERR_PAGED_RANGE).  Two rows with the same slot: one of them is kept, which is not defined.
  * d as fa_fwd.  Rows that are 16-byte aligned (base and stride) with rot_dim a multiple of 16
  * take the vector path; any others work, slower.
