@@ -83,8 +83,7 @@ __device__ __forceinline__ uint16_t narrow(float x) {
 // Shared set-up of both kernels: which of the CTA's tokens are there, where their cache rows are
 // (elements; -1: left out), and their angles.
 template <int TOK>
-__device__ __forceinline__ void stage_tokens(const RopeParams &p, long long t0, long long (&row)[TOK],
-                                             float2 *angles) {
+__device__ __forceinline__ void stage_tokens(const RopeParams &p, long long t0, long long (&row)[TOK], float2 *angles) {
     const int tid = int(threadIdx.x), half = p.rot / 2;
     if (tid < TOK) {
         const long long t = t0 + tid;
@@ -102,16 +101,17 @@ __device__ __forceinline__ void stage_tokens(const RopeParams &p, long long t0, 
         }
         row[tid] = at;
     }
+    // Token fastest: a warp's lanes then share few pairs (the parameters are read one address at a time).
 #pragma unroll 1
     for (int w = tid; w < TOK * half; w += int(blockDim.x)) {
-        const int tok = w / half, i = w - tok * half;
+        const int i = w / TOK, tok = w % TOK;
         const long long t = t0 + tok;
         if (t < p.T) {
             double turn = double(p.positions[p.axis[i] * p.pos_stride + t]) * p.turns[i];
             turn -= rint(turn);
             float s, c;
             sincospif(2.f * float(turn), &s, &c);
-            angles[w] = make_float2(c, p.sin_sign * s);
+            angles[tok * (half + 1) + i] = make_float2(c, p.sin_sign * s);   // (padded: the lanes' tokens in other banks)
         }
     }
     __syncthreads();
@@ -149,7 +149,7 @@ __device__ __forceinline__ Lane head_lane(const RopeParams &p, int h, long long 
 // head: for the rotated part 8 pairs (two runs of 8 values rot/2 apart, or one run of 16
 // interleaved), else 16 values that are copied.
 template <bool F16, int TOK>
-__global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 2) fa_rope_kernel(const __grid_constant__ RopeParams p) {
     extern __shared__ float2 angles[];
     __shared__ long long row[TOK];
     const long long t0 = (long long)blockIdx.x * TOK;
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const __grid_cons
             uint32_t a[4] = {x[tok][0].x, x[tok][0].y, x[tok][0].z, x[tok][0].w};
             uint32_t b[4] = {x[tok][1].x, x[tok][1].y, x[tok][1].z, x[tok][1].w};
             if (turn) {
-                const float2 *cs = angles + tok * half + a0;
+                const float2 *cs = angles + tok * (half + 1) + a0;
                 if (split) {
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_any_kernel(const __grid_
 
 template <bool F16>
 int launch(const RopeParams &p, bool vec, int num_sms, cudaStream_t st) {
-    const size_t per_token = size_t(p.rot / 2) * sizeof(float2);
+    const size_t per_token = size_t(p.rot / 2 + 1) * sizeof(float2);
     const int heads = p.Hq + p.Hkv + (p.v_cache != nullptr ? p.Hkv : 0);
     const int units = vec ? heads * (p.d / 16) : heads * (p.d - p.rot / 2), rounds = (units + kRopeThreads - 1) / kRopeThreads;
     const unsigned threads = unsigned(((units + rounds - 1) / rounds + 31) / 32 * 32);

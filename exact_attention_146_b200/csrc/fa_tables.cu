@@ -12,7 +12,9 @@
 // launch, one round trip for the lengths, one for the table entries.  One thread-block cluster of
 // up to eight CTAs runs it; every CTA sums all lengths itself (no exchange), takes every n-th
 // token, and the cluster barrier orders the reads of the lengths and the free count before their
-// updated values are written, which is what lets both be updated in place.
+// updated values are written, which is what lets both be updated in place.  A step of many tokens
+// goes over the whole GPU instead, and a second small kernel, set up meanwhile, writes those values
+// (1500 requests, 100,000 tokens: see the launch).
 #include <algorithm>
 #include <cstdint>
 
@@ -30,49 +32,40 @@ namespace cg = cooperative_groups;
 
 constexpr int kTableThreads = 1024;
 constexpr int kMaxCluster = 8;
+constexpr int kMostItems = 1 << 30;   // requests, tokens, blocks: strided loops stay within 32 bits
+// Tokens up to which one cluster does a step.
+constexpr int kClusterTokens = 16384;
 constexpr int kBatch = 4;   // tokens or blocks a thread has in flight
 
-// Inclusive scan over the block of a pair of sums packed in 64 bits (low: tokens, high: blocks;
-// each below 2^31, so the halves never carry).  `warp_sums`: 32 words of shared memory.
-__device__ __forceinline__ unsigned long long block_scan(unsigned long long x, unsigned long long *warp_sums,
-                                                         unsigned long long *total) {
-    const int lane = int(threadIdx.x) % 32, warp = int(threadIdx.x) / 32, warps = int(blockDim.x) / 32;
+__device__ __forceinline__ int blocks_of(int tokens, int page) {   // tokens + page - 1 may pass 2^31
+    return int((unsigned(tokens) + unsigned(page) - 1u) / unsigned(page));
+}
+
+// Inclusive scan over a warp.
+__device__ __forceinline__ unsigned long long warp_scan(unsigned long long x) {
+    const int lane = int(threadIdx.x) % 32;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
         const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
-    __syncthreads();   // the previous scan's sums have been read
-    if (lane == 31) warp_sums[warp] = x;
-    __syncthreads();
-    unsigned long long before = 0, all = 0;
-    for (int w = 0; w < warps; ++w) {
-        const unsigned long long s = warp_sums[w];
-        if (w < warp) before += s;
-        all += s;
-    }
-    *total = all;
-    return x + before;
+    return x;
 }
 
-// Sum of one 64-bit value and OR of one flag over the block.
-__device__ __forceinline__ void block_total(long long &a, long long &b, int &flag, long long *buf) {
+// Inclusive scan over the block of a pair of sums packed in 64 bits (low: tokens, high: blocks;
+// each below 2^31, so the halves never carry).  `warp_sums`: 32 words of shared memory; `flag` becomes
+// its OR over the block.
+__device__ __forceinline__ unsigned long long block_scan(unsigned long long x, unsigned long long *warp_sums,
+                                                         unsigned long long *total, int &flag) {
     const int lane = int(threadIdx.x) % 32, warp = int(threadIdx.x) / 32, warps = int(blockDim.x) / 32;
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
-    if (lane == 0) {
-        buf[warp] = a;
-        buf[32 + warp] = b;
-    }
+    x = warp_scan(x);
+    __syncthreads();   // the previous scan's sums have been read
+    if (lane == 31) warp_sums[warp] = x;
     flag = __syncthreads_or(flag);
-    a = b = 0;
-    for (int w = 0; w < warps; ++w) {
-        a += buf[w];
-        b += buf[32 + w];
-    }
+    const unsigned long long upto = warp_scan(lane < warps ? warp_sums[lane] : 0ull);   // each warp scans them again
+    *total = __shfl_sync(0xffffffffu, upto, 31);
+    const unsigned long long before = __shfl_sync(0xffffffffu, upto, (warp + 31) % 32);
+    return x + (warp > 0 ? before : 0ull);
 }
 
 // The last entry of `starts` (ascending, n entries, starts[0] <= x) that is <= x: the request that
@@ -102,57 +95,84 @@ struct ReserveParams {
     int R, T, max_blocks, num_blocks, page;
 };
 
+// What a launch does: all of it by one cluster, the tokens and the table by any grid, or the values
+// that may be updated in place (after that grid) by one CTA.
+enum class ReservePart { All, Tokens, Lengths };
+
+template <ReservePart PART>
 __global__ void __launch_bounds__(kTableThreads) fa_kv_reserve_kernel(const __grid_constant__ ReserveParams p) {
-    __shared__ unsigned long long warp_sums[64];
+    __shared__ unsigned long long warp_sums[32];
     __shared__ int s_cu[kTableThreads], s_off[kTableThreads], s_ctx[kTableThreads], s_held[kTableThreads];
-    cg::cluster_group cluster = cg::this_cluster();
-    const int rank = int(cluster.block_rank()), ranks = int(cluster.num_blocks());
+    if (PART == ReservePart::Tokens) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int rank = int(blockIdx.x), ranks = int(gridDim.x);   // (the cluster is the grid)
     const int tid = int(threadIdx.x), nt = int(blockDim.x);
     const int count = *p.free_count;
 
-    // Totals, and whether every length fits: a step that does not fit is refused whole.
+    // Totals, and whether every length fits: a step that does not fit is refused whole.  (Sums that
+    // leave 31 bits are caught by the running check: no step has that many tokens or blocks.)
     long long tokens = 0, blocks = 0;
     int bad = 0;
     int ctx0 = 0, new0 = 0;   // this thread's request of the first chunk
-    for (int r = tid; r < p.R; r += nt) {
-        const int c = p.ctx[r], n = p.fresh[r];
-        if (r == tid) ctx0 = c, new0 = n;
-        if (c < 0 || n < 0 || (long long)c + n > (long long)p.max_blocks * p.page) {
-            if (!bad && rank == 0) report_range(p.status, kSiteLengths, r);
-            bad = 1;
+    unsigned long long upto0 = 0, total0 = 0;
+    for (int base = 0; base < p.R; base += nt) {
+        const int r = base + tid;
+        const int c = r < p.R ? p.ctx[r] : 0, n = r < p.R ? p.fresh[r] : 0;
+        unsigned long long mine = 0;
+        int off = 0;
+        if (c < 0 || n < 0 || (long long)c + n > (long long)p.max_blocks * p.page || n > p.T) {
+            off = 1;
+            if (rank == 0 && PART != ReservePart::Lengths)
+                report_range(p.status, n > p.T && c >= 0 ? kSiteTokens : kSiteLengths, r);
         } else {
-            tokens += n;
-            blocks += (c + n + p.page - 1LL) / p.page - (c + p.page - 1LL) / p.page;
+            mine = (unsigned long long)(unsigned)n | ((unsigned long long)(unsigned)(blocks_of(c + n, p.page) - blocks_of(c, p.page)) << 32);
         }
+        unsigned long long total = 0;
+        const unsigned long long upto = block_scan(mine, warp_sums, &total, off);
+        bad |= off;
+        tokens += (long long)(total & 0xffffffffu);
+        blocks += (long long)(total >> 32);
+        if (base == 0) ctx0 = c, new0 = n, upto0 = upto - mine, total0 = total;
     }
-    block_total(tokens, blocks, bad, reinterpret_cast<long long *>(warp_sums));
     if (!bad && tokens > p.T) {
         bad = 1;
-        if (rank == 0 && tid == 0) report_range(p.status, kSiteTokens, 0);
+        if (rank == 0 && tid == 0 && PART != ReservePart::Lengths) report_range(p.status, kSiteTokens, 0);
     }
     if (!bad && (count < 0 || count > p.num_blocks || blocks > count)) {
         bad = 1;
-        if (rank == 0 && tid == 0) report_range(p.status, kSiteBlocks, 0);
+        if (rank == 0 && tid == 0 && PART != ReservePart::Lengths) report_range(p.status, kSiteBlocks, 0);
     }
 
+    // the lengths have been read; and this kernel ends after the tokens' one
+    if (PART == ReservePart::Lengths) asm volatile("griddepcontrol.wait;" ::: "memory");
     int tok_base = 0, blk_base = 0;
     if (!bad) {
         for (int base = 0; base < p.R; base += nt) {
             const int r = base + tid, n_here = min(nt, p.R - base);
             const int c = base == 0 ? ctx0 : (r < p.R ? p.ctx[r] : 0);
             const int n = base == 0 ? new0 : (r < p.R ? p.fresh[r] : 0);
-            const int held = int((c + p.page - 1LL) / p.page);
-            const int need = int(((long long)c + n + p.page - 1) / p.page) - held;
-            const unsigned long long mine = (unsigned long long)(unsigned)n | ((unsigned long long)(unsigned)need << 32);
-            unsigned long long total = 0;
-            const unsigned long long upto = block_scan(mine, warp_sums, &total) - mine;
+            const int held = blocks_of(c, p.page);
+            unsigned long long upto = upto0, total = total0;
+            if (base > 0) {
+                const unsigned long long mine = (unsigned long long)(unsigned)n | ((unsigned long long)(unsigned)(blocks_of(c + n, p.page) - held) << 32);
+                int none = 0;
+                upto = block_scan(mine, warp_sums, &total, none) - mine;
+            }
+            const int tok_end = tok_base + int(total & 0xffffffffu), blk_end = blk_base + int(total >> 32);
+            if (PART == ReservePart::Lengths) {
+                if (r < p.R) {
+                    p.cu[r] = tok_base + int(upto & 0xffffffffu);
+                    p.seq_lens[r] = c + n;
+                }
+                tok_base = tok_end;
+                blk_base = blk_end;
+                continue;
+            }
             s_cu[tid] = tok_base + int(upto & 0xffffffffu);
             s_off[tid] = blk_base + int(upto >> 32);
             s_ctx[tid] = c;
             s_held[tid] = held;
-            if (rank == 0 && r < p.R) p.cu[r] = s_cu[tid];
+            if (PART == ReservePart::All && rank == 0 && r < p.R) p.cu[r] = s_cu[tid];
             __syncthreads();
-            const int tok_end = tok_base + int(total & 0xffffffffu), blk_end = blk_base + int(total >> 32);
             // kBatch tokens a thread at a time: their searches and loads overlap
             const int step = ranks * nt;
             for (int t0 = tok_base + rank * nt + tid; t0 < tok_end; t0 += kBatch * step) {
@@ -192,20 +212,26 @@ __global__ void __launch_bounds__(kTableThreads) fa_kv_reserve_kernel(const __gr
             blk_base = blk_end;
             __syncthreads();
         }
-    } else if (rank == 0) {
-        for (int r = tid; r < p.R; r += nt) p.cu[r] = 0;
-    }
-    for (int t = tok_base + rank * nt + tid; t < p.T; t += ranks * nt) {
-        p.positions[t] = 0;
-        p.slots[t] = -1;
-    }
-    cluster.sync();   // every CTA has read the lengths and the count: they may be updated in place
-    if (rank == 0) {
-        for (int r = tid; r < p.R; r += nt) p.seq_lens[r] = bad ? p.ctx[r] : p.ctx[r] + p.fresh[r];
-        if (tid == 0) {
-            p.cu[p.R] = tok_base;
-            *p.free_count_out = count - blk_base;
+    } else if (PART != ReservePart::Tokens && rank == 0) {
+        for (int r = tid; r < p.R; r += nt) {
+            p.cu[r] = 0;
+            if (PART == ReservePart::Lengths) p.seq_lens[r] = p.ctx[r];
         }
+    }
+    if (PART != ReservePart::Lengths)
+        for (int t = tok_base + rank * nt + tid; t < p.T; t += ranks * nt) {
+            p.positions[t] = 0;
+            p.slots[t] = -1;
+        }
+    if (PART == ReservePart::Tokens) return;
+    if (PART == ReservePart::All) {
+        cg::this_cluster().sync();   // every CTA has read the lengths and the count: they may be updated in place
+        if (rank == 0)
+            for (int r = tid; r < p.R; r += nt) p.seq_lens[r] = bad ? p.ctx[r] : p.ctx[r] + p.fresh[r];
+    }
+    if (rank == 0 && tid == 0) {
+        p.cu[p.R] = tok_base;
+        *p.free_count_out = count - blk_base;
     }
 }
 
@@ -222,26 +248,34 @@ struct ReleaseParams {
 };
 
 __global__ void __launch_bounds__(kTableThreads) fa_kv_release_kernel(const __grid_constant__ ReleaseParams p) {
-    __shared__ unsigned long long warp_sums[64];
+    __shared__ unsigned long long warp_sums[32];
     __shared__ int s_off[kTableThreads];
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = int(cluster.block_rank()), ranks = int(cluster.num_blocks());
     const int tid = int(threadIdx.x), nt = int(blockDim.x);
     const int count = *p.free_count;
 
-    long long blocks = 0, unused = 0;
+    long long blocks = 0;
     int bad = 0;
-    for (int r = tid; r < p.R; r += nt) {
-        const int n = p.lens[r];
-        if (p.done[r] == 0) continue;
-        if (n < 0 || n > (long long)p.max_blocks * p.page) {
-            if (!bad && rank == 0) report_range(p.status, kSiteLengths, r);
-            bad = 1;
-        } else {
-            blocks += (n + p.page - 1LL) / p.page;
+    unsigned long long upto0 = 0, total0 = 0;
+    for (int base = 0; base < p.R; base += nt) {
+        const int r = base + tid;
+        int held = 0, off = 0;
+        if (r < p.R && p.done[r] != 0) {
+            const int n = p.lens[r];
+            if (n < 0 || n > (long long)p.max_blocks * p.page) {
+                off = 1;
+                if (rank == 0) report_range(p.status, kSiteLengths, r);
+            } else {
+                held = blocks_of(n, p.page);
+            }
         }
+        unsigned long long total = 0;
+        const unsigned long long upto = block_scan((unsigned long long)(unsigned)held, warp_sums, &total, off);
+        bad |= off;
+        blocks += (long long)total;
+        if (base == 0) upto0 = upto - (unsigned)held, total0 = total;
     }
-    block_total(blocks, unused, bad, reinterpret_cast<long long *>(warp_sums));
     if (!bad && (count < 0 || count + blocks > p.num_blocks)) {   // more blocks than the stack can hold
         bad = 1;
         if (rank == 0 && tid == 0) report_range(p.status, kSiteBlocks, 0);
@@ -250,10 +284,13 @@ __global__ void __launch_bounds__(kTableThreads) fa_kv_release_kernel(const __gr
     if (!bad) {
         for (int base = 0; base < p.R; base += nt) {
             const int r = base + tid, n_here = min(nt, p.R - base);
-            const int held = (r < p.R && p.done[r] != 0) ? int((p.lens[r] + p.page - 1LL) / p.page) : 0;
-            unsigned long long total = 0;
-            const unsigned long long upto = block_scan((unsigned long long)(unsigned)held, warp_sums, &total);
-            s_off[tid] = blk_base + int(upto) - held;
+            unsigned long long upto = upto0, total = total0;
+            if (base > 0) {
+                const int held = (r < p.R && p.done[r] != 0) ? blocks_of(p.lens[r], p.page) : 0;
+                int none = 0;
+                upto = block_scan((unsigned long long)(unsigned)held, warp_sums, &total, none) - (unsigned)held;
+            }
+            s_off[tid] = blk_base + int(upto);
             __syncthreads();
             const int blk_end = blk_base + int(total);
             const int step = ranks * nt;
@@ -323,6 +360,7 @@ int fa_kv_reserve(const int *ctx_lens, const int *new_lens, int R, int *block_ta
                   void *stream) {
     if (R < 0 || T < 0 || max_blocks < 0 || num_blocks < 0 || page_size < 1) return FA_ERR_INVALID_ARG;
     if (table_stride < max_blocks) return FA_ERR_INVALID_ARG;
+    if (std::max({R, T, num_blocks}) > kMostItems) return FA_ERR_INVALID_ARG;
     if ((long long)max_blocks * page_size > 0x7fffffffLL) return FA_ERR_INVALID_ARG;   // lengths are 32-bit
     const size_t lens_b = size_t(R) * 4, tab_b = max_blocks > 0 ? table_bytes(R, table_stride, max_blocks) : 0;
     const size_t free_b = size_t(num_blocks) * 4, cu_b = (size_t(R) + 1) * 4, pos_b = size_t(T) * 4, slot_b = size_t(T) * 8;
@@ -360,7 +398,25 @@ int fa_kv_reserve(const int *ctx_lens, const int *new_lens, int R, int *block_ta
     p.max_blocks = max_blocks;
     p.num_blocks = num_blocks;
     p.page = page_size;
-    return launch_cluster(fa_kv_reserve_kernel, p, std::max(R, T), R, static_cast<cudaStream_t>(stream));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T <= kClusterTokens) return launch_cluster(fa_kv_reserve_kernel<ReservePart::All>, p, std::max(R, T), R, st);
+    const unsigned ctas = unsigned(std::min((T + 4 * kTableThreads - 1) / (4 * kTableThreads) * 4, dev->num_sms));
+    fa_kv_reserve_kernel<ReservePart::Tokens><<<ctas, kTableThreads, 0, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kTableThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;   // set up while the tokens are written
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, fa_kv_reserve_kernel<ReservePart::Lengths>, p) != cudaSuccess) {
+        cudaGetLastError();
+        return FA_ERR_CUDA;
+    }
+    return FA_OK;
 }
 
 int fa_kv_release(const int *lens, const int *done, int R, const int *block_table, long long table_stride,
@@ -368,6 +424,7 @@ int fa_kv_release(const int *lens, const int *done, int R, const int *block_tabl
                   int *lens_out, int *free_count_out, void *stream) {
     if (R < 0 || max_blocks < 0 || num_blocks < 0 || page_size < 1) return FA_ERR_INVALID_ARG;
     if (table_stride < max_blocks) return FA_ERR_INVALID_ARG;
+    if (std::max({R, num_blocks}) > kMostItems) return FA_ERR_INVALID_ARG;
     if ((long long)max_blocks * page_size > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
     const size_t lens_b = size_t(R) * 4, tab_b = max_blocks > 0 ? table_bytes(R, table_stride, max_blocks) : 0;
     const size_t free_b = size_t(num_blocks) * 4;

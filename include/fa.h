@@ -298,7 +298,7 @@ int fa_merge_partials(const float *o_parts, const float *lse_parts, int R, void 
  *   lens[r] for the others (lens_out may be lens, free_count_out may be free_count).  The table
  *   is not changed.  Lengths out of range, or more blocks than num_blocks in the stack: refused
  *   whole, as above.
- * R, T, max_blocks, num_blocks >= 0, page_size >= 1, max_blocks * page_size < 2^31.  int32 arrays
+ * 0 <= R, T, num_blocks <= 2^30, max_blocks >= 0, page_size >= 1, max_blocks * page_size < 2^31.  int32 arrays
  * 4-byte aligned, slots 8-byte; empty arrays may be NULL.
  */
 int fa_kv_reserve(const int *ctx_lens, const int *new_lens, int R, int *block_table, long long table_stride,

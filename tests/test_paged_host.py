@@ -24,7 +24,7 @@ def reserve(L, ctx=A[0], new=A[1], R=4, table=A[2], stride=8, max_blocks=8, free
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(R=-1), 1), (dict(T=-1), 1), (dict(page=0), 1), (dict(blocks=-1), 1), (dict(max_blocks=-1), 1), (dict(stride=7), 1),
+    (dict(R=-1), 1), (dict(T=-1), 1), (dict(T=(1 << 30) + 1), 1), (dict(blocks=(1 << 30) + 1), 1), (dict(page=0), 1), (dict(blocks=-1), 1), (dict(max_blocks=-1), 1), (dict(stride=7), 1),
     (dict(max_blocks=1 << 28, stride=1 << 28), 1), (dict(cu=None), 1), (dict(count=None), 1), (dict(out=None), 1), (dict(ctx=None), 1),
     (dict(new=None), 1), (dict(lens=None), 1), (dict(table=None), 1), (dict(free=None), 1), (dict(pos=None), 1), (dict(slots=None), 1),
     (dict(slots=A[8] + 4), 3), (dict(pos=A[7] + 2), 3), (dict(ctx=A[0] + 1), 3), (dict(lens=A[1]), 8), (dict(lens=A[0] + 4), 8),
