@@ -171,7 +171,7 @@ template <bool H> using Tile256 = TileCfg<256, 64, 1, 4, 1, 2, false, 0, H>;
 // (d = 128, 8 requests of up to 512 new tokens, 352 units).
 constexpr int kTileOverhead = 3;
 
-template <class C>
+template <class C, int FEW>
 int launch_tiles(const PagedParams &base, const View &q, const View &kv, int few, char *workspace, int ctas, int dev,
                  cudaStream_t st) {
     static int state[kMaxDevices] = {};
@@ -200,7 +200,7 @@ int launch_tiles(const PagedParams &base, const View &q, const View &kv, int few
     PagedParams pf = base;
     pf.plan.n_hi = few;
     pf.say = 0;
-    if (few > 0 && (rc = launch_rows<C::D, C::F16, kRowRows>(pf, kv, workspace, ctas, dev, st)) != FA_OK) return rc;
+    if (few > 0 && (rc = launch_rows<C::D, C::F16, FEW>(pf, kv, workspace, ctas, dev, st)) != FA_OK) return rc;
     if (few > 0) {   // beside the kernel before it, which began when the inputs were complete
         rc = launch_after(fa_paged_tiles_kernel<C>, unsigned(ctas), C::THREADS, PlanSmem<C>::BYTES, st, mq, mk, mv, p);
         if (rc != FA_OK) return rc;
@@ -210,21 +210,21 @@ int launch_tiles(const PagedParams &base, const View &q, const View &kv, int few
     }
     const int blocks = (ctas - 1) * (rows / 32) + (few > 0 ? pf.plan.workers - 1 : 0);
     if (blocks == 0) return FA_OK;
-    return launch_after(fa_paged_merge_kernel<C>, unsigned(blocks), 256, 0, st, p, pf);
+    return launch_after(fa_paged_merge_kernel<C, FEW>, unsigned(blocks), 256, 0, st, p, pf);
 }
 
-template <bool F16>
+template <bool F16, int FEW>
 int dispatch_tiles(PagedParams p, const View &kv, int d, int few, char *workspace, int ctas, int dev, cudaStream_t st) {
     p.pack = largest_divisor(p.n_rep, kBlockQ);
     const View q{p.q, {p.Hq, p.plan.T, 1}, {d, p.q_stride, p.q_stride * p.plan.T}, {p.pack, kBlockQ / p.pack, 1}};
     switch (d) {
-        case 32: return launch_tiles<Tile32<F16>>(p, q, kv, few, workspace, ctas, dev, st);
-        case 64: return launch_tiles<Tile64<F16>>(p, q, kv, few, workspace, ctas, dev, st);
-        case 80: return launch_tiles<Tile80<F16>>(p, q, kv, few, workspace, ctas, dev, st);
-        case 96: return launch_tiles<Tile96<F16>>(p, q, kv, few, workspace, ctas, dev, st);
-        case 128: return launch_tiles<Tile128<F16>>(p, q, kv, few, workspace, ctas, dev, st);
-        case 192: return launch_tiles<Tile192<F16>>(p, q, kv, few, workspace, ctas, dev, st);
-        default: return launch_tiles<Tile256<F16>>(p, q, kv, few, workspace, ctas, dev, st);
+        case 32: return launch_tiles<Tile32<F16>, FEW>(p, q, kv, few, workspace, ctas, dev, st);
+        case 64: return launch_tiles<Tile64<F16>, FEW>(p, q, kv, few, workspace, ctas, dev, st);
+        case 80: return launch_tiles<Tile80<F16>, FEW>(p, q, kv, few, workspace, ctas, dev, st);
+        case 96: return launch_tiles<Tile96<F16>, FEW>(p, q, kv, few, workspace, ctas, dev, st);
+        case 128: return launch_tiles<Tile128<F16>, FEW>(p, q, kv, few, workspace, ctas, dev, st);
+        case 192: return launch_tiles<Tile192<F16>, FEW>(p, q, kv, few, workspace, ctas, dev, st);
+        default: return launch_tiles<Tile256<F16>, FEW>(p, q, kv, few, workspace, ctas, dev, st);
     }
 }
 
@@ -310,11 +310,15 @@ int paged_fwd(const void *q, long long q_stride, const fa_paged_cache *cache, co
     char *const ws = static_cast<char *>(workspace);
     // Row tiles of 128 need pages of whole swizzle atoms (8 slots); any other page, and calls of few rows,
     // take the kernel that gathers key by key.  In a mixed call the requests of few rows take it too.
-    const int few = kRowRows / p.n_rep;   // new tokens whose rows fit it
+    const bool eight = p.n_rep <= 8;   // a unit of 8 rows holds a decoding step; else one of 16
+    const int few = kRowRows / p.n_rep;   // new tokens whose rows fit a unit
     if (max_new > few && p.page % 8 == 0 && p.num_blocks > 0) {
-        const int split = R > 1 ? few : 0;
-        return f16 ? dispatch_tiles<true>(p, kv, d, split, ws, ctas, dev_id, st)
-                   : dispatch_tiles<false>(p, kv, d, split, ws, ctas, dev_id, st);
+        const int split = R == 1 ? 0 : eight ? 8 / p.n_rep : few;
+        if (eight)
+            return f16 ? dispatch_tiles<true, 8>(p, kv, d, split, ws, ctas, dev_id, st)
+                       : dispatch_tiles<false, 8>(p, kv, d, split, ws, ctas, dev_id, st);
+        return f16 ? dispatch_tiles<true, kRowRows>(p, kv, d, split, ws, ctas, dev_id, st)
+                   : dispatch_tiles<false, kRowRows>(p, kv, d, split, ws, ctas, dev_id, st);
     }
     // Rows are the narrow side of the kernel's products: 8 where they fit (a decoding step of up to 8 heads a KV
     // head), which halves the products.

@@ -473,7 +473,7 @@ fa_paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 
 // The merge after the tile kernel: blocks of 32 rows a cut, then (where the call has a kernel of few
 // rows too) that one's cuts.
-template <class C>
+template <class C, int FEW>
 __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_constant__ PagedTileParams p,
                                                              const __grid_constant__ PagedParams few) {
     constexpr int kRows = C::NQT * kBlockQ, kPer = kRows / 32;
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(256) fa_paged_merge_kernel(const __grid_consta
         if (job.parts > 0)
             merge_unit<C::D, C::F16, kRows, kBlockQ>(p, job, w, i % kPer * 32, 32, [&](int s) { return p.cuts[w - 1 + s] < p.cuts[w + s]; });
     } else {
-        merge_rows<C::D, C::F16, kRowRows>(few, i - tile_blocks + 1);
+        merge_rows<C::D, C::F16, FEW>(few, i - tile_blocks + 1);
     }
 }
 

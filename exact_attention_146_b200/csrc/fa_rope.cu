@@ -145,15 +145,33 @@ __device__ __forceinline__ Lane head_lane(const RopeParams &p, int h, long long 
     return l;
 }
 
-// Vector path: rot and d multiples of 16, every row 16-byte aligned.  A unit is 16 values of one
-// head: for the rotated part 8 pairs (two runs of 8 values rot/2 apart, or one run of 16
-// interleaved), else 16 values that are copied.
-template <bool F16, int TOK>
+// N words of a row, one vector.
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&x)[N], const uint16_t *src) {
+    if constexpr (N == 4) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(src));
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(src));
+        x[0] = v.x, x[1] = v.y;
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_words(uint16_t *dst, const uint32_t (&x)[N]) {
+    if constexpr (N == 4) *reinterpret_cast<uint4 *>(dst) = make_uint4(x[0], x[1], x[2], x[3]);
+    else *reinterpret_cast<uint2 *>(dst) = make_uint2(x[0], x[1]);
+}
+
+// Vector path: every row 16-byte aligned, and rot a multiple of 2 W (W = 8, or 4 where rot / 2 is an odd
+// number of fours).  A unit is 2 W values of one head: for the rotated part W pairs (two runs of W
+// values rot/2 apart, or one run of 2 W interleaved), else 2 W values that are copied.
+template <bool F16, int TOK, int W>
 __global__ void __launch_bounds__(kRopeThreads, 2) fa_rope_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int N = W / 2;   // words a run
     extern __shared__ float2 angles[];
     __shared__ long long row[TOK];
     const long long t0 = (long long)blockIdx.x * TOK;
-    const int half = p.rot / 2, per_head = p.d / 16;
+    const int half = p.rot / 2, per_head = p.d / (2 * W);
     const int heads = p.Hq + p.Hkv + (p.v_cache != nullptr ? p.Hkv : 0), units = heads * per_head;
     const int here = int(min((long long)TOK, p.T - t0));   // tokens of this CTA
     bool staged = false;
@@ -161,16 +179,16 @@ __global__ void __launch_bounds__(kRopeThreads, 2) fa_rope_kernel(const __grid_c
         const int h = u / per_head, i = u - h * per_head;
         Lane l{};
         if (u < units) l = head_lane(p, h, t0);
-        const bool turn = l.turn && 16 * i < p.rot;
+        const bool turn = l.turn && 2 * W * i < p.rot;
         const bool split = turn && p.interleaved == 0;
-        const int e0 = split ? 8 * i : 16 * i, e1 = split ? half + 8 * i : 16 * i + 8;
-        const int a0 = 8 * i;   // first pair of the unit
-        uint4 x[TOK][2];
+        const int e0 = split ? W * i : 2 * W * i, e1 = split ? half + W * i : 2 * W * i + W;
+        const int a0 = W * i;   // first pair of the unit
+        uint32_t x[TOK][2][N];
 #pragma unroll
         for (int tok = 0; tok < TOK; ++tok) {
             if (u < units && tok < here) {
-                x[tok][0] = __ldcs(reinterpret_cast<const uint4 *>(l.src + tok * l.src_stride + e0));
-                x[tok][1] = __ldcs(reinterpret_cast<const uint4 *>(l.src + tok * l.src_stride + e1));
+                load_words<N>(x[tok][0], l.src + tok * l.src_stride + e0);
+                load_words<N>(x[tok][1], l.src + tok * l.src_stride + e1);
             }
         }
         if (!staged) {   // (every thread comes here once: in its first round, with a unit or without)
@@ -181,31 +199,26 @@ __global__ void __launch_bounds__(kRopeThreads, 2) fa_rope_kernel(const __grid_c
 #pragma unroll
         for (int tok = 0; tok < TOK; ++tok) {
             if (row[tok] < 0) continue;
-            uint32_t a[4] = {x[tok][0].x, x[tok][0].y, x[tok][0].z, x[tok][0].w};
-            uint32_t b[4] = {x[tok][1].x, x[tok][1].y, x[tok][1].z, x[tok][1].w};
+            uint32_t (&a)[N] = x[tok][0], (&b)[N] = x[tok][1];
             if (turn) {
                 const float2 *cs = angles + tok * (half + 1) + a0;
-                if (split) {
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const float2 lo = unpack<F16>(a[w]), hi = unpack<F16>(b[w]);
+                for (int w = 0; w < N; ++w) {
+                    const float2 lo = unpack<F16>(a[w]), hi = unpack<F16>(b[w]);
+                    if (split) {
                         const float2 r0 = cs[2 * w], r1 = cs[2 * w + 1];
                         a[w] = pack<F16>(lo.x * r0.x - hi.x * r0.y, lo.y * r1.x - hi.y * r1.y);
                         b[w] = pack<F16>(hi.x * r0.x + lo.x * r0.y, hi.y * r1.x + lo.y * r1.y);
-                    }
-                } else {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const float2 lo = unpack<F16>(a[w]), hi = unpack<F16>(b[w]);
-                        const float2 r0 = cs[w], r1 = cs[4 + w];
+                    } else {
+                        const float2 r0 = cs[w], r1 = cs[N + w];
                         a[w] = pack<F16>(lo.x * r0.x - lo.y * r0.y, lo.y * r0.x + lo.x * r0.y);
                         b[w] = pack<F16>(hi.x * r1.x - hi.y * r1.y, hi.y * r1.x + hi.x * r1.y);
                     }
                 }
             }
             uint16_t *dst = l.dst + (l.cache ? row[tok] : tok * l.dst_stride);
-            *reinterpret_cast<uint4 *>(dst + e0) = make_uint4(a[0], a[1], a[2], a[3]);
-            *reinterpret_cast<uint4 *>(dst + e1) = make_uint4(b[0], b[1], b[2], b[3]);
+            store_words<N>(dst + e0, a);
+            store_words<N>(dst + e1, b);
         }
     }
 }
@@ -244,20 +257,26 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_any_kernel(const __grid_
     }
 }
 
+template <bool F16, int W>
+void launch_vec(const RopeParams &p, int num_sms, unsigned threads, size_t per_token, cudaStream_t st) {
+    if (p.T <= 4 * num_sms) {
+        fa_rope_kernel<F16, 1, W><<<unsigned(p.T), threads, per_token, st>>>(p);
+    } else {
+        constexpr int TOK = kRopeTokens;
+        fa_rope_kernel<F16, TOK, W><<<unsigned((p.T + TOK - 1) / TOK), threads, TOK * per_token, st>>>(p);
+    }
+}
+
 template <bool F16>
 int launch(const RopeParams &p, bool vec, int num_sms, cudaStream_t st) {
     const size_t per_token = size_t(p.rot / 2 + 1) * sizeof(float2);
-    const int heads = p.Hq + p.Hkv + (p.v_cache != nullptr ? p.Hkv : 0);
-    const int units = vec ? heads * (p.d / 16) : heads * (p.d - p.rot / 2), rounds = (units + kRopeThreads - 1) / kRopeThreads;
+    const int heads = p.Hq + p.Hkv + (p.v_cache != nullptr ? p.Hkv : 0), width = p.rot % 16 == 0 ? 8 : 4;
+    vec = vec && p.rot % 8 == 0;
+    const int units = vec ? heads * (p.d / (2 * width)) : heads * (p.d - p.rot / 2), rounds = (units + kRopeThreads - 1) / kRopeThreads;
     const unsigned threads = unsigned(((units + rounds - 1) / rounds + 31) / 32 * 32);
-    if (!vec) {
-        fa_rope_any_kernel<F16><<<unsigned(p.T), threads, per_token, st>>>(p);
-    } else if (p.T <= 4 * num_sms) {
-        fa_rope_kernel<F16, 1><<<unsigned(p.T), threads, per_token, st>>>(p);
-    } else {
-        constexpr int TOK = kRopeTokens;
-        fa_rope_kernel<F16, TOK><<<unsigned((p.T + TOK - 1) / TOK), threads, TOK * per_token, st>>>(p);
-    }
+    if (!vec) fa_rope_any_kernel<F16><<<unsigned(p.T), threads, per_token, st>>>(p);
+    else if (width == 8) launch_vec<F16, 8>(p, num_sms, threads, per_token, st);
+    else launch_vec<F16, 4>(p, num_sms, threads, per_token, st);
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -342,7 +361,7 @@ int rope(const void *q, long long q_stride, void *q_out, long long qo_stride, in
     p.d = d;
     p.page = 1;
     fill_spec(&p, spec, inverse);
-    const bool vec = p.rot % 16 == 0 && (Hq == 0 || (vec_rows(q, q_stride) && vec_rows(q_out, qo_stride))) &&
+    const bool vec = (Hq == 0 || (vec_rows(q, q_stride) && vec_rows(q_out, qo_stride))) &&
                      (Hkv == 0 || (vec_rows(k, k_stride) && vec_rows(k_out, ko_stride)));
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     return f16 ? launch<true>(p, vec, dev->num_sms, st) : launch<false>(p, vec, dev->num_sms, st);
@@ -411,7 +430,7 @@ int rope_append(const void *q, long long q_stride, void *q_out, long long qo_str
     p.d = d;
     p.page = cache->page_size;
     fill_spec(&p, spec, 0);
-    const bool vec = p.rot % 16 == 0 && (Hq == 0 || (vec_rows(q, q_stride) && vec_rows(q_out, qo_stride))) &&
+    const bool vec = (Hq == 0 || (vec_rows(q, q_stride) && vec_rows(q_out, qo_stride))) &&
                      vec_rows(k, k_stride) && vec_rows(v, v_stride);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     return f16 ? launch<true>(p, vec, dev->num_sms, st) : launch<false>(p, vec, dev->num_sms, st);

@@ -350,8 +350,8 @@ typedef struct fa_rope_spec {
  *   slots[t] / page_size of the cache.  Rows with a negative slot are left out: nothing
  *   of theirs is written, q_out included.  A slot >= num_blocks * page_size is left out too and reported
  *   (FA_ERR_PAGED_RANGE).  Two rows with the same slot: one of them is kept, which is not defined.
- * d as fa_fwd.  Rows that are 16-byte aligned (base and stride) with rot_dim a multiple of 16
- * take the vector path; any others work, slower.
+ * d as fa_fwd.  Rows that are 16-byte aligned (base and stride) with rot_dim a multiple of 8
+ * take the vector paths; any others work, slower.
  */
 int fa_rope(const void *q, long long q_stride, void *q_out, long long qo_stride, int Hq, const void *k,
             long long k_stride, void *k_out, long long ko_stride, int Hkv, int T, int d, const int *positions,

@@ -133,6 +133,7 @@ ROPE = [(torch.bfloat16, 128, 128, 1, False, 1, 4, 2), (torch.float16, 128, 64, 
         (torch.bfloat16, 80, 80, 3, False, 33, 16, 16), (torch.bfloat16, 80, 20, 3, True, 129, 5, 1),
         (torch.float16, 32, 32, 4, False, 1000, 1, 1), (torch.bfloat16, 64, 6, 1, False, 3, 2, 2),
         (torch.float16, 256, 256, 1, True, 601, 8, 1), (torch.bfloat16, 192, 96, 3, False, 64, 6, 2),
+        (torch.bfloat16, 80, 40, 1, False, 700, 6, 2), (torch.float16, 80, 40, 2, True, 9, 3, 3),
         (torch.bfloat16, 96, 0, 1, False, 5, 2, 1), (torch.float16, 96, 96, 1, True, 2500, 2, 0)]
 
 
@@ -199,7 +200,7 @@ def test_rope_of_unaligned_rows(shift):
     close(fa.fa_rope(x, pos, table), want, _paged.rope_tolerance(x, want, 32, False))
 
 
-@pytest.mark.parametrize("dtype,d,rot,axes,pairs,T,Hq,Hkv", ROPE[:9])
+@pytest.mark.parametrize("dtype,d,rot,axes,pairs,T,Hq,Hkv", ROPE[:11])
 @pytest.mark.parametrize("layout", ["nhd", "hnd", "pair"])
 def test_rope_append(dtype, d, rot, axes, pairs, T, Hq, Hkv, layout):
     torch.manual_seed(T + d + 1)
