@@ -96,7 +96,8 @@ struct View {
 };
 
 // Chunks on the tensor cores; requests of at most `few` new tokens (few > 0) by the kernel of few rows
-// before it, in the same stream but not in its way: the tile kernel's CTAs start as the other's end.
+// behind it, whose CTAs start as the tile kernel's end: those end up to a quarter of the time apart, and the
+// other's work fills that.
 // The caches as the tensor maps see them: the axes after d, the nearer of head and slot first.
 View cache_view(const PagedParams &p, int Hkv) {
     View kv{p.k, {Hkv, p.page, p.num_blocks}, {p.head_stride, p.slot_stride, p.block_stride}, {1, 1, 1}};
@@ -122,7 +123,7 @@ constexpr int kRowOverhead = 2;
 
 // The kernel of few rows; fills what it adds to `p`.
 template <class C>
-int launch_rows_as(PagedParams &p, const View &kv, char *workspace, int ctas, int dev, cudaStream_t st) {
+int launch_rows_as(PagedParams &p, const View &kv, bool after_tiles, char *workspace, int ctas, int dev, cudaStream_t st) {
     static int state[kMaxDevices] = {};
     int rc = make_ready(fa_paged_rows_kernel<C>, C::SMEM, 0, state[dev]);
     if (rc != FA_OK) return rc;
@@ -139,20 +140,22 @@ int launch_rows_as(PagedParams &p, const View &kv, char *workspace, int ctas, in
     p.o_part = reinterpret_cast<float *>(workspace);
     p.lse_part = reinterpret_cast<float *>(workspace + part_o_bytes(p.plan.workers, C::ROWS, C::D));
     p.jobs = reinterpret_cast<MergeJob *>(workspace + part_bytes(p.plan.workers, C::ROWS, C::D));
+    // after the tile kernel, which began when the inputs were complete: beside its last CTAs
+    if (after_tiles) return launch_after(fa_paged_rows_kernel<C>, unsigned(ctas), C::THREADS, C::SMEM, st, mk, mv, p);
     fa_paged_rows_kernel<C><<<unsigned(ctas), C::THREADS, C::SMEM, st>>>(mk, mv, p);
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 // Pages of whole swizzle atoms come by TMA, any other row by row.
 template <int D, bool F16, int ROWS>
-int launch_rows(PagedParams &p, const View &kv, char *workspace, int ctas, int dev, cudaStream_t st) {
-    return p.page % 8 == 0 && p.num_blocks > 0 ? launch_rows_as<RowsOf<D, F16, ROWS, true>>(p, kv, workspace, ctas, dev, st)
-                                               : launch_rows_as<RowsOf<D, F16, ROWS, false>>(p, kv, workspace, ctas, dev, st);
+int launch_rows(PagedParams &p, const View &kv, bool after_tiles, char *workspace, int ctas, int dev, cudaStream_t st) {
+    return p.page % 8 == 0 && p.num_blocks > 0 ? launch_rows_as<RowsOf<D, F16, ROWS, true>>(p, kv, after_tiles, workspace, ctas, dev, st)
+                                               : launch_rows_as<RowsOf<D, F16, ROWS, false>>(p, kv, after_tiles, workspace, ctas, dev, st);
 }
 
 template <int D, bool F16, int ROWS>
 int launch_rows_only(PagedParams p, const View &kv, char *workspace, int ctas, int dev, cudaStream_t st) {
-    const int rc = launch_rows<D, F16, ROWS>(p, kv, workspace, ctas, dev, st);
+    const int rc = launch_rows<D, F16, ROWS>(p, kv, false, workspace, ctas, dev, st);
     if (rc != FA_OK) return rc;
     return launch_after(fa_paged_merge_rows_kernel<D, F16, ROWS>, unsigned(p.plan.workers - 1), 256, 0, st, p);
 }
@@ -200,14 +203,9 @@ int launch_tiles(const PagedParams &base, const View &q, const View &kv, int few
     PagedParams pf = base;
     pf.plan.n_hi = few;
     pf.say = 0;
-    if (few > 0 && (rc = launch_rows<C::D, C::F16, FEW>(pf, kv, workspace, ctas, dev, st)) != FA_OK) return rc;
-    if (few > 0) {   // beside the kernel before it, which began when the inputs were complete
-        rc = launch_after(fa_paged_tiles_kernel<C>, unsigned(ctas), C::THREADS, PlanSmem<C>::BYTES, st, mq, mk, mv, p);
-        if (rc != FA_OK) return rc;
-    } else {
-        fa_paged_tiles_kernel<C><<<unsigned(ctas), C::THREADS, PlanSmem<C>::BYTES, st>>>(mq, mk, mv, p);
-        if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-    }
+    fa_paged_tiles_kernel<C><<<unsigned(ctas), C::THREADS, PlanSmem<C>::BYTES, st>>>(mq, mk, mv, p);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    if (few > 0 && (rc = launch_rows<C::D, C::F16, FEW>(pf, kv, true, workspace, ctas, dev, st)) != FA_OK) return rc;
     const int blocks = (ctas - 1) * (rows / 32) + (few > 0 ? pf.plan.workers - 1 : 0);
     if (blocks == 0) return FA_OK;
     return launch_after(fa_paged_merge_kernel<C, FEW>, unsigned(blocks), 256, 0, st, p, pf);

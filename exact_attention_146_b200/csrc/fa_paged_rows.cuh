@@ -272,6 +272,7 @@ fa_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     const long long x0 = start_of(worker), x1 = start_of(worker + 1);
     if (x0 >= x1) {
         if (lane == 0) p.jobs[worker].parts = 0;
+        asm volatile("griddepcontrol.wait;" ::: "memory");   // (see the end)
         return;
     }
 
@@ -415,6 +416,7 @@ fa_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                 // gives up: the copies still on their way land before the warp ends (the last ones of each slot)
                 for (int s = 0; s < C::STAGES; ++s)
                     if (s != get) wait_rows(bars + 8u * s, s > get ? parity : parity ^ 1u, p.plan.status);
+                asm volatile("griddepcontrol.wait;" ::: "memory");
                 return;
             }
             send();   // into the slot that the step before this one used
@@ -564,6 +566,7 @@ fa_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             }
         }
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // ends after the tile kernel that it may run beside
 }
 
 // Merges the pieces of the unit that cut w crosses first: rows row0 .. row0 + rows - 1 of it, by the

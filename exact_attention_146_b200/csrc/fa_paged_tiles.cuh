@@ -407,7 +407,8 @@ fa_paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::SMEM_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + C::SMEM_MISC + 4);
     const Ctl ctl{abort_flag, p.plan.status, kWaitLimitNs};
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge may be set up meanwhile
+    // The few-rows kernel of a mixed call takes the SMs as this one's CTAs end; then the merge.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (threadIdx.x == 0) {
         init_barriers<C>(sbase);
@@ -468,7 +469,6 @@ fa_paged_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     __syncthreads();
     sm100::tc_fence_after_sync();
     if (warp == 0) sm100::tmem_dealloc(tmem, C::TMEM_COLS);
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // ends after the kernel of few rows that it may run beside
 }
 
 // The merge after the tile kernel: blocks of 32 rows a cut, then (where the call has a kernel of few
