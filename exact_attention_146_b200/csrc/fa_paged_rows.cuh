@@ -228,7 +228,7 @@ fa_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ PlanScan<C::THREADS> scan;
     __shared__ uint64_t landed[C::WARPS][C::STAGES];   // a step's rows are in their slot
-    __shared__ Place places[C::WARPS];
+    __shared__ int segment[C::WARPS];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge may be set up meanwhile
     const int tid = int(threadIdx.x), lane = tid % 32, warp = tid / 32;
     if (C::TMA && tid == 0) {
@@ -258,13 +258,12 @@ fa_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     // Neighbouring workers are on different SMs, so that few of them spread out.
     auto worker_of = [&](int w) { return w * int(gridDim.x) + int(blockIdx.x); };
     auto start_of = [&](int i) { return i < workers ? i * share + min((long long)i, more) : total; };
-    {   // the thread whose requests hold a worker's first step finds it
+    {   // the thread whose requests hold a worker's first step says so
         const long long from = scan.seg_start[tid], to = scan.seg_start[tid + 1];
-#pragma unroll 1
+#pragma unroll
         for (int w = 0; w < C::WARPS; ++w) {
             const long long x = start_of(worker_of(w));
-            if (x >= from && x < to)
-                places[w] = find_request<C::KEYS>(plan, scan.seg_start, tid, (plan.R + C::THREADS - 1) / C::THREADS, x);
+            if (x >= from && x < to) segment[w] = tid;
         }
     }
     __syncthreads();
@@ -277,7 +276,7 @@ fa_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     }
 
     Walk walk{};                // the computing side's
-    walk.u = find_unit<C::KEYS>(plan, places[warp], x0);
+    walk.u = find_unit<C::KEYS>(plan, find_request<C::KEYS>(plan, scan.seg_start, segment[warp], (plan.R + C::THREADS - 1) / C::THREADS, x0), x0);
     walk.o = x0 - walk.u.begin;
     walk.left = x1 - x0;
     walk.first = true;

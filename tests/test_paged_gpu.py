@@ -430,6 +430,98 @@ def test_on_a_stream_of_its_own(new):
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
 
 
+def test_offsets_beyond_32_bits():
+    """A cache of more than 2^32 elements: its last blocks are written and read."""
+    page, Hkv, d = 16, 8, 128
+    blocks = (1 << 32) // (page * Hkv * d) + 40
+    k_cache = torch.empty((blocks, page, Hkv, d), dtype=torch.bfloat16, device="cuda")
+    v_cache = torch.empty_like(k_cache)
+    n = 70
+    ids = torch.arange(blocks - 5, blocks, device="cuda")
+    t = torch.arange(n, device="cuda")
+    slots = ids[t // page] * page + t % page
+    q, k, v = (torch.randn(n, h, d, device="cuda").to(torch.bfloat16) for h in (16, Hkv, Hkv))
+    inv, axis = spec(d, 1)
+    fa.fa_rope_append(None, k, v, t.int(), fa.RopeTable(inv), k_cache, v_cache, slots)
+    want = _paged.rope64(k, t[None], inv, axis, False)
+    close(k_cache[ids].reshape(-1, Hkv, d)[:n], want, _paged.rope_tolerance(k, want, d // 2, False))
+    assert torch.equal(v_cache[ids].reshape(-1, Hkv, d)[:n], v)
+    table = torch.full((1, 5), 0, dtype=torch.int32, device="cuda")
+    table[0] = ids.int()
+    v_cache[ids[-1], n % page:] = float("nan")   # behind the last key
+    for new in (1, 60):
+        out, _ = fa.fa_paged_fwd(q[:new], k_cache, v_cache, table, i32([0, new]), i32([n]), max_new=new)
+        want, _, t_out, _ = _paged.attend64(q[:new], k_cache[ids], v_cache[ids], torch.arange(5, device="cuda")[None], [0, new], [n],
+                                            causal=True, window=None, scale=d ** -0.5)
+        close(out, want, t_out)
+
+
+def mixed_problem(seed, d=128):
+    lens = [300, 1, 900, 64, 2000, 17]
+    news = [1, 1, 300, 2, 70, 0]
+    k, v, table = _paged.make_paged(lens, 16, 2, d, torch.bfloat16, "nhd", seed)
+    q = torch.randn(sum(news), 8, d, device="cuda").to(torch.bfloat16)
+    cu = [0]
+    for n in news:
+        cu.append(cu[-1] + n)
+    return (q, k, v, table, i32(cu), i32(lens)), dict(max_new=300)
+
+
+def test_two_calls_at_once_and_one_after_the_other():
+    """Calls on two streams, each with its own workspace, and calls in one stream that share one."""
+    args, kw = zip(*(mixed_problem(s) for s in (1, 2)))
+    alone = [fa.fa_paged_fwd(*a, **w) for a, w in zip(args, kw)]
+    need = fa.paged_workspace_bytes(8, 2, 128)
+    ws = [torch.empty(need, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.empty_like(a[0]) for _ in range(20)] for a in args]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for x in range(2):
+            fa.fa_paged_fwd(*args[x], **kw[x], out=outs[x][i], return_lse=False, workspace=ws[x], stream=streams[x])
+    torch.cuda.synchronize()
+    for x in range(2):
+        assert all(torch.equal(o, alone[x][0]) for o in outs[x])
+    for i in range(20):
+        fa.fa_paged_fwd(*args[i % 2], **kw[i % 2], out=outs[i % 2][i], return_lse=False, workspace=ws[0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(outs[i % 2][i], alone[i % 2][0]) for i in range(20))
+
+
+def test_mixed_call_captured_and_replayed():
+    """Chunks and decoding requests in one captured call, replayed on new values and new lengths."""
+    args, kw = mixed_problem(3)
+    q, k, v, table, cu, lens = args
+    ws = torch.empty(fa.paged_workspace_bytes(8, 2, 128), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(8, q.shape[0], device="cuda")
+    fa.fa_paged_fwd(*args, **kw, out=out, lse=lse, workspace=ws)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        fa.fa_paged_fwd(*args, **kw, out=out, lse=lse, workspace=ws)
+    for shift in (0, 1, 40):
+        q.normal_()
+        lens.copy_(i32([300 - shift, 1, 900 - shift, 64 - shift, 2000 - shift, 17]))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = fa.fa_paged_fwd(*args, **kw)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_the_same_block_twice():
+    """Two requests that share their first blocks (a common prefix), and one that names a block twice."""
+    k, v, table = _paged.make_paged([200], 16, 2, 64, torch.bfloat16, "nhd", 5)
+    table = torch.cat([table, table, table])
+    table[2, 3] = table[2, 1]
+    lens, news = [200, 130, 200], [1, 60, 3]
+    q = torch.randn(sum(news), 4, 64, device="cuda").to(torch.bfloat16)
+    cu = [0, 1, 61, 64]
+    out, _ = fa.fa_paged_fwd(q, k, v, table, i32(cu), i32(lens), max_new=60)
+    want, _, t_out, _ = _paged.attend64(q, k, v, table, cu, lens, causal=True, window=None, scale=0.125)
+    close(out, want, t_out)
+
+
 # ------------------------------------------------------------------------------- together
 
 def test_serving_loop_matches_dense_attention():
