@@ -47,6 +47,15 @@ inline bool rows_overlap(const Rows &a, const Rows &b, int T, int es) {
     return off < uintptr_t(a.width) * es || off + uintptr_t(b.width) * es > step;
 }
 
+// The strides of axes of one entry mean nothing: they become d, which every rule allows.
+inline fa_paged_cache tidy_cache(const fa_paged_cache &given) {
+    fa_paged_cache c = given;
+    if (c.num_blocks <= 1) c.block_stride = c.d;
+    if (c.page_size <= 1) c.slot_stride = c.d;
+    if (c.Hkv <= 1) c.head_stride = c.d;
+    return c;
+}
+
 // Bytes from the cache's base to the end of its last element (k and v alike).
 inline size_t cache_bytes(const fa_paged_cache *c) {
     if (c->num_blocks == 0) return 0;
@@ -58,8 +67,7 @@ inline int valid_cache(const fa_paged_cache *c) {
     if (c->num_blocks < 0 || c->page_size < 1 || c->Hkv < 1 || c->Hkv > 65535) return FA_ERR_INVALID_ARG;
     if (fa_tile_config(c->d, nullptr, nullptr, nullptr, nullptr) != FA_OK) return FA_ERR_UNSUPPORTED_HEAD_DIM;
     if (c->block_stride % 8 != 0 || c->slot_stride % 8 != 0 || c->head_stride % 8 != 0) return FA_ERR_INVALID_ARG;
-    // axes from the innermost out: each stride spans all that lies inside it (axes of one
-    // entry take part too, so a stride is never smaller than the head's row)
+    // axes from the innermost out: each stride spans all that lies inside it
     struct Axis { long long stride, n; } ax[3] = {{c->block_stride, c->num_blocks}, {c->slot_stride, c->page_size},
                                                   {c->head_stride, c->Hkv}};
     std::sort(ax, ax + 3, [](const Axis &a, const Axis &b) { return a.stride < b.stride; });

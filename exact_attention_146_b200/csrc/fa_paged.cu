@@ -245,18 +245,20 @@ int dispatch_rows(const PagedParams &p, const View &kv, int d, char *workspace, 
     }
 }
 
-int paged_fwd(const void *q, long long q_stride, const fa_paged_cache *cache, const int *block_table,
+int paged_fwd(const void *q, long long q_stride, const fa_paged_cache *given, const int *block_table,
               long long table_stride, int max_blocks, const int *cu_seqlens, const int *seq_lens, int R, int T, int Hq,
               int max_new, float scale, int causal, int window, void *out, float *lse, void *workspace,
               size_t workspace_bytes, bool f16, void *stream) {
     // ---- host-only validation
-    if (cache == nullptr || R < 0 || T < 0 || Hq <= 0 || Hq > 65535 || max_new < 0 || max_blocks < 0) return FA_ERR_INVALID_ARG;
+    if (given == nullptr || R < 0 || T < 0 || Hq <= 0 || Hq > 65535 || max_new < 0 || max_blocks < 0) return FA_ERR_INVALID_ARG;
+    const fa_paged_cache tidy = tidy_cache(*given), *cache = &tidy;
     int rc = valid_cache(cache);
     if (rc != FA_OK) return rc;
     const int d = cache->d, Hkv = cache->Hkv;
     if (Hq % Hkv != 0 || (causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal)) return FA_ERR_INVALID_ARG;
     if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
-    if (table_stride < max_blocks || (long long)max_blocks * cache->page_size > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+    if (table_stride < max_blocks || (long long)max_blocks * cache->page_size > 0x7fffffffLL - 4096)
+        return FA_ERR_INVALID_ARG;   // (keys of the last tile stay within 32 bits)
     if (q_stride < (long long)Hq * d || q_stride % 8 != 0) return FA_ERR_INVALID_ARG;
     if (R == 0 || T == 0) return FA_OK;
     const size_t q_b = (size_t(T - 1) * size_t(q_stride) + size_t(Hq) * d) * 2, out_b = size_t(T) * Hq * d * 2;

@@ -369,8 +369,9 @@ int rope(const void *q, long long q_stride, void *q_out, long long qo_stride, in
 
 int rope_append(const void *q, long long q_stride, void *q_out, long long qo_stride, int Hq, const void *k,
                 long long k_stride, const void *v, long long v_stride, int T, const int *positions, long long pos_stride,
-                const fa_rope_spec *spec, const fa_paged_cache *cache, const long long *slots, bool f16, void *stream) {
-    if (T < 0 || Hq < 0 || spec == nullptr || cache == nullptr) return FA_ERR_INVALID_ARG;
+                const fa_rope_spec *spec, const fa_paged_cache *given, const long long *slots, bool f16, void *stream) {
+    if (T < 0 || Hq < 0 || spec == nullptr || given == nullptr) return FA_ERR_INVALID_ARG;
+    const fa_paged_cache tidy = tidy_cache(*given), *cache = &tidy;
     const int rc0 = valid_cache(cache);
     if (rc0 != FA_OK) return rc0;
     const int d = cache->d, Hkv = cache->Hkv;

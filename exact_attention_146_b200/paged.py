@@ -353,16 +353,17 @@ class PagedKV:
         self.free_count = torch.full((1,), num_blocks, **ints)
         self.cu_seqlens = torch.zeros(max_requests + 1, **ints)
         self.positions = self.slots = None
+        self._rows = {}   # num_tokens -> (positions, slots): kept, so that a captured step's buffers stay its own
 
     def reserve(self, new_lens, num_tokens: int, *, stream=None):
         """Room for new_lens [max_requests] int32 more tokens, num_tokens rows in all (rows behind the last
         token are allowed: a captured step of fixed size).  Returns positions and slots."""
         if self.tables is not self:
             raise ValueError("reserve on the layer that holds the tables")
-        torch = _Types.torch
-        if self.slots is None or self.slots.numel() != num_tokens:
-            self.positions = _empty((num_tokens,), torch.int32, self.seq_lens.device, stream)
-            self.slots = _empty((num_tokens,), torch.int64, self.seq_lens.device, stream)
+        if num_tokens not in self._rows:
+            self._rows[num_tokens] = (_empty((num_tokens,), _Types.i32, self.seq_lens.device, stream),
+                                      _empty((num_tokens,), _Types.i64, self.seq_lens.device, stream))
+        self.positions, self.slots = self._rows[num_tokens]
         fa_kv_reserve(self.seq_lens, new_lens, self.block_table, self.free_blocks, self.free_count, page_size=self.page_size,
                       cu_seqlens=self.cu_seqlens, seq_lens=self.seq_lens, positions=self.positions, slots=self.slots,
                       free_count_out=self.free_count, stream=stream)

@@ -294,7 +294,8 @@ int fa_merge_partials(const float *o_parts, const float *lse_parts, int R, void 
  *   the free count unchanged).  A block id outside 0 .. num_blocks - 1, in the table or the free
  *   stack, is reported the same way; tokens in such a block get slot -1.
  * fa_kv_release: every request with done[r] != 0 gives back its ceil(lens[r] / page_size) blocks,
- *   pushed on the free stack in table order, requests in order; lens_out[r] = 0 for those and
+ *   pushed on the free stack in table order, requests in order (a block that two tables name is
+ *   pushed by each: who shares blocks between requests counts their users); lens_out[r] = 0 for those and
  *   lens[r] for the others (lens_out may be lens, free_count_out may be free_count).  The table
  *   is not changed.  Lengths out of range, or more blocks than num_blocks in the stack: refused
  *   whole, as above.
@@ -314,7 +315,8 @@ int fa_kv_release(const int *lens, const int *done, int R, const int *block_tabl
  * k[b * block_stride + s * slot_stride + h * head_stride + e] (strides in elements, multiples of
  * 8; 16-byte aligned bases; v likewise), so a block may keep its slots together per head
  * ([block, head, slot, d]) or its heads together per slot ([block, slot, head, d]).  No two
- * (b, s, h) may share memory: each of the three strides is >= the extent of the ones inside it.
+ * (b, s, h) may share memory: each of the three strides is >= the extent of the ones inside it
+ * (the stride of an axis of one entry is not looked at).
  */
 typedef struct fa_paged_cache {
     void *k, *v;                                      /* bf16 or fp16, device memory */
@@ -377,7 +379,7 @@ int fa_rope_append_f16(const void *q, long long q_stride, void *q_out, long long
  *   block_table [R, max_blocks] (rows table_stride apart), cu_seqlens [R + 1], seq_lens [R]:
  *       int32 device arrays; seq_lens[r] = L_r keys in all, the new tokens' own among them
  *   out [T, Hq, d] dense, 16-byte aligned;  lse [Hq, T] fp32 natural log, or NULL
- *   max_new: an upper bound of n_r, known on the host
+ *   max_new: an upper bound of n_r, known on the host;  max_blocks * page_size < 2^31 - 4096
  *
  * New token i of request r sees key j < L_r iff (causal = 0 or j <= i + L_r - n_r) and
  * (window = 0 or j > i + L_r - n_r - window); window > 0 needs causal = 1.  A row that sees no
@@ -431,7 +433,7 @@ const char *fa_status_string(int status);
  * device's kernel status word: FA_OK, FA_ERR_DEVICE_TIMEOUT if a pipeline wait in a
  * forward or backward kernel ran out of time, or FA_ERR_PAGED_RANGE (the first report is
  * kept).  FA_ERR_CUDA if the synchronisation itself failed.  If `detail` is not NULL it
- * receives the raw status word (bits 8..15 name the wait: 1-12 forward, 21-34 backward; bits
+ * receives the raw status word (bits 8..15 name the wait: 1-16 forward, 21-34 backward; bits
  * 16.. the CTA; for FA_ERR_PAGED_RANGE bits 8..15: 41 lengths, 42 tokens, 43 free blocks, 44 a
  * free-stack entry, 45 a table entry, 46 a slot; bits 16.. the request, or the token of a slot).
  */

@@ -456,6 +456,19 @@ def test_offsets_beyond_32_bits():
         close(out, want, t_out)
 
 
+def test_strides_of_axes_of_one_entry():
+    """One KV head, or one block, in a tensor whose stride there is anything."""
+    base = torch.randn(4, 16, 3, 64, device="cuda").to(torch.bfloat16)
+    k = torch.as_strided(base, (4, 16, 1, 64), (16 * 192, 192, 7, 1), 64)
+    v = torch.as_strided(base, (4, 16, 1, 64), (16 * 192, 192, 7, 1), 128)
+    table = i32([[2, 0, 3, 1]])
+    for new in (1, 40):
+        q = torch.randn(new, 2, 64, device="cuda").to(torch.bfloat16)
+        out, _ = fa.fa_paged_fwd(q, k, v, table, i32([0, new]), i32([60]), max_new=new)
+        want, _, t_out, _ = _paged.attend64(q, k, v, table, [0, new], [60], causal=True, window=None, scale=0.125)
+        close(out, want, t_out)
+
+
 def mixed_problem(seed, d=128):
     lens = [300, 1, 900, 64, 2000, 17]
     news = [1, 1, 300, 2, 70, 0]

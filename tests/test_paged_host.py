@@ -120,6 +120,8 @@ def test_append_accepts(L):
     assert append(L, c=cache(bs=2 * n, ss=4 * 128, v=A[10] + 4 * 128)) in NO_DEVICE
     assert append(L, c=cache(bs=2 * n - 2 * 128, ss=4 * 128, v=A[10] + 4 * 128)) == fa.FA_ERR_OVERLAP   # v's last row on the next block
     assert append(L, c=cache(bs=2 * n, v=A[10] + 2 * n - 256)) == fa.FA_ERR_OVERLAP
+    # strides of axes of one entry mean nothing
+    assert append(L, c=cache(Hkv=1, hs=3, bs=16 * 128, ss=128)) in NO_DEVICE and append(L, c=cache(n=1, bs=5)) in NO_DEVICE
 
 
 def attend(L, q=A[0], qs=512, c=None, table=A[1], stride=8, max_blocks=8, cu=A[2], lens=A[3], R=4, T=9, Hq=4, max_new=3, scale=0.1, causal=1,
@@ -132,7 +134,8 @@ def attend(L, q=A[0], qs=512, c=None, table=A[1], stride=8, max_blocks=8, cu=A[2
 @pytest.mark.parametrize("kw,code", [
     (dict(R=-1), 1), (dict(T=-1), 1), (dict(Hq=3), 1), (dict(Hq=0), 1), (dict(max_new=-1), 1), (dict(qs=504), 1), (dict(qs=516), 1),
     (dict(scale=0.0), 1), (dict(scale=float("nan")), 1), (dict(causal=2), 1), (dict(window=-1), 1), (dict(causal=0, window=4), 1),
-    (dict(stride=7), 1), (dict(max_blocks=1 << 28, stride=1 << 28), 1), (dict(q=None), 1), (dict(out=None), 1), (dict(cu=None), 1),
+    (dict(stride=7), 1), (dict(max_blocks=1 << 28, stride=1 << 28), 1), (dict(max_blocks=(1 << 27) - 1, stride=1 << 27), 1),
+    (dict(q=None), 1), (dict(out=None), 1), (dict(cu=None), 1),
     (dict(lens=None), 1), (dict(table=None), 1), (dict(ws=None), 1), (dict(ws_bytes=1000), 1), (dict(ws=A[6] + 128), 3),
     (dict(q=A[0] + 8), 3), (dict(out=A[4] + 2), 3), (dict(lse=A[5] + 2), 3), (dict(out=A[0]), 8), (dict(lse=A[4]), 8), (dict(ws=A[10]), 8),
     (dict(out=A[11]), 8), (dict(lse=A[1]), 8)] + [(dict(c=cache(**kw)), code) for kw, code in CACHES if kw != dict(v=A[10] + 256)])
