@@ -221,15 +221,10 @@ __device__ inline long long plan_scan(const PlanParams &p, PlanScan<NT> &sh, int
     return total;
 }
 
-// First step of worker w's range, and the worker that step x belongs to.
+// First step of worker w's range.
 FA_PLAN long long range_start(long long total, int workers, int w) {
     const long long q = div_pos(total, workers), rem = total - q * workers;
     return w * q + min((long long)w, rem);
-}
-FA_PLAN int range_owner(long long total, int workers, long long x) {
-    const long long q = div_pos(total, workers), rem = total - q * workers;
-    if (x < rem * (q + 1)) return int(div_pos(x, q + 1));
-    return int(rem + div_pos(x - rem * (q + 1), q));
 }
 
 // What the merge is told of one cut: the unit that it crosses first (parts = 0: none), its pieces

@@ -3,7 +3,7 @@
 //
 // Few rows make it a matter of reading K and V once: 4 d flops a key and row against 4 d bytes a
 // key, at most 16 flops a byte, where the card's rates cross at about 250.  So every warp is a
-// worker of its own: it takes one contiguous range of 16-key steps (fa_paged_plan.cuh), streams
+// worker of its own: it takes one contiguous range of steps of 16 or 32 keys (fa_paged_plan.cuh), streams
 // the keys' rows into its own ring in shared memory, and never waits for another warp; nothing but
 // the ring's depth limits the bytes in flight.  Pages of whole swizzle atoms (8 slots) come by TMA, a
 // box a page or the largest power-of-two run of slots that divides it; any other page row by row, a bulk
@@ -16,9 +16,12 @@
 // softmax down each column, and O^T (d x rows) += V^T P^T, all in registers with the warp-level m16n8k16
 // product.  The rows are its narrow side (8, or 2 x 8): an MMA of 128 rows would be 15/16 empty here, and
 // the other way round (rows as the 16) a decoding step of up to 8 rows took twice the products.  The
-// transposed operands cost nothing: V^T comes from ldmatrix.trans, P^T from one movmatrix per 8 keys.  At the end of a unit the warp writes O / l and LSE, or, where a cut of the
-// line crosses the unit, its own normalised O and LSE to the workspace (fp32); the merge kernel
-// combines those in the order of the workers:  LSE = ln sum_s e^LSE_s,  O = sum_s e^(LSE_s - LSE) O_s.
+// transposed operands cost nothing: V^T comes from ldmatrix.trans, P^T from one movmatrix per 8 keys.
+// m, l, S and O are fp32; P is rounded to the inputs' type for the second product (its operands have one
+// type; the error is half a step of each weight, and l sums the unrounded values), O once at the end.
+//
+// At the end of a unit the warp writes O / l and LSE, or, where a cut of the line crosses the unit, its
+// own normalised O and LSE to the workspace (fp32); the merge kernel combines those in the order of the workers:  LSE = ln sum_s e^LSE_s,  O = sum_s e^(LSE_s - LSE) O_s.
 //
 // Measured (B200, in a CUDA graph): 48 requests of 4k to 16k keys (Hq 32, Hkv 8, d 128) 247 us, 6.56 TB/s (the measured copy
 // rate is 6.55); 4 requests of up to 1000 keys 11.6 us: the plan 4, the first copies 2, the merge 3.

@@ -101,7 +101,6 @@ template <int KS, int NT> int check(std::mt19937 &rng, int round) {
         const long long x0 = range_start(total, p.workers, w), x1 = range_start(total, p.workers, w + 1);
         if (x0 != x || x1 < x0 || x1 - x0 > total / p.workers + 1) return 7;
         if (x1 == x0) continue;
-        if (range_owner(total, p.workers, x0) != w || range_owner(total, p.workers, x1 - 1) != w) return 8;
         Unit u = plan_find<KS>(p, sh.seg_start, NT, seg, x0);
         while (x < x1) {
             while (begin[k + 1] <= x) ++k;
