@@ -85,12 +85,10 @@ FA_PLAN long long floor_sum_from(long long nb, long long m, long long a, long lo
     return floor_sum(nb, m, a, c);
 }
 
-// Request r; one that is out of range counts as having no tokens (and is reported once).
-FA_PLAN Request load_request(const PlanParams &p, int r, bool say = false) {
-    Request q;
-    q.q0 = p.cu[r];
-    q.n = p.cu[r + 1] - q.q0;
-    q.L = p.lens[r];
+// Request r of rows q0 .. end - 1 and L keys; one that is out of range counts as having no tokens (and
+// is reported once).
+FA_PLAN Request make_request(const PlanParams &p, int r, int q0, int end, int L, bool say) {
+    Request q{q0, end - q0, L};
     if (q.q0 < 0 || q.n < 0 || q.n > p.max_new || (long long)q.q0 + q.n > p.T || q.L < 0 || (long long)q.L > p.max_len) {
 #ifdef __CUDA_ARCH__
         if (say) fa_host::report_range(p.status, fa_host::kSiteLengths, r);
@@ -100,6 +98,7 @@ FA_PLAN Request load_request(const PlanParams &p, int r, bool say = false) {
     if (q.n < p.n_lo || q.n > p.n_hi) q.n = 0;
     return q;
 }
+FA_PLAN Request load_request(const PlanParams &p, int r) { return make_request(p, r, p.cu[r], p.cu[r + 1], p.lens[r], false); }
 
 FA_PLAN int plan_blocks(const PlanParams &p, const Request &q) { return (q.n + p.tpb - 1) / p.tpb; }
 
@@ -175,11 +174,23 @@ __device__ inline long long plan_scan(const PlanParams &p, PlanScan<NT> &sh, int
     const int seg = (p.R + NT - 1) / NT, lane = tid % 32, warp = tid / 32;
     long long steps = 0;
     int units = 0;
-    for (int r = tid * seg; r < min(p.R, (tid + 1) * seg); ++r) {
-        const Request q = load_request(p, r, say);
-        if (q.n > 0) {
-            steps += p.groups * plan_steps<KS>(p, q, plan_blocks(p, q));
-            units += plan_units(p, q);
+    const int last = min(p.R, (tid + 1) * seg);
+    for (int r0 = tid * seg; r0 < last; r0 += 4) {   // the loads of four requests together
+        int cu[5], L[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            cu[k] = p.cu[min(r0 + k, last)];
+            L[k] = p.lens[min(r0 + k, last - 1)];
+        }
+        cu[4] = p.cu[min(r0 + 4, last)];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (r0 + k >= last) break;
+            const Request q = make_request(p, r0 + k, cu[k], cu[k + 1], L[k], say);
+            if (q.n > 0) {
+                steps += p.groups * plan_steps<KS>(p, q, plan_blocks(p, q));
+                units += plan_units(p, q);
+            }
         }
     }
     long long upto = steps;
