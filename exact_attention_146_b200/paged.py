@@ -81,6 +81,11 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _like(t, shape, stream):
+    """An uninitialised buffer of t's type on its device."""
+    return t.new_empty(shape) if stream is None else _empty(shape, t.dtype, t.device, stream)
+
+
 def _ints(name, t, n, dtype=None):
     """The pointer of a contiguous 1-D CUDA tensor of n int32 (or dtype)."""
     dtype = dtype or _Types.i32
@@ -172,7 +177,7 @@ def fa_rope(q, positions, table: RopeTable, *, k=None, inverse: bool = False, q_
     shape = q.shape
     T, Hq, d = shape
     if q_out is None:
-        q_out = _empty(shape, dtype, q.device, stream)
+        q_out = _like(q, shape, stream)
     qo, qos = _rows("q_out", q_out, dtype, shape)
     kp = ko = None
     ks = kos = Hkv = 0
@@ -183,7 +188,7 @@ def fa_rope(q, positions, table: RopeTable, *, k=None, inverse: bool = False, q_
         if shape[0] != T or shape[2] != d:
             raise ValueError(f"k must be [{T}, heads, {d}], got {tuple(shape)}")
         if k_out is None:
-            k_out = _empty(shape, dtype, q.device, stream)
+            k_out = _like(k, shape, stream)
         ko, kos = _rows("k_out", k_out, dtype, shape)
     spec, pos, ps = table._spec(positions, T)
     _run("fa_rope" + f16, stream, qp, qs, qo, qos, Hq, kp, ks, ko, kos, Hkv, T, d, pos, ps, spec, 1 if inverse else 0)
@@ -211,7 +216,7 @@ def fa_rope_append(q, k, v, positions, table: RopeTable, k_cache, v_cache, slots
         if shape[0] != T or shape[2] != d:
             raise ValueError(f"q must be [{T}, heads, {d}], got {tuple(shape)}")
         if q_out is None:
-            q_out = _empty(shape, dtype, q.device, stream)
+            q_out = _like(q, shape, stream)
         qo, qos = _rows("q_out", q_out, dtype, shape)
     spec, pos, ps = table._spec(positions, T)
     _run("fa_rope_append" + f16, stream, qp, qs, qo, qos, Hq, kp, ks, vp, vs, T, pos, ps, spec, ctypes.byref(c),
@@ -297,7 +302,7 @@ def fa_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, *, max_
     R = seq_lens.numel()
     table, stride, width = _table(block_table, R)
     if out is None:
-        out = _empty(shape, dtype, q.device, stream)
+        out = _like(q, shape, stream)
     elif out.dtype is not dtype or out.shape != shape or not out.is_contiguous():
         raise ValueError(f"out must be contiguous {dtype} {tuple(shape)}, got {out.dtype} {tuple(out.shape)}")
     lse_p = None
