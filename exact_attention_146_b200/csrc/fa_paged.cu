@@ -259,7 +259,7 @@ int paged_fwd(const void *q, long long q_stride, const fa_paged_cache *given, co
     const int d = cache->d, Hkv = cache->Hkv;
     if (Hq % Hkv != 0 || (causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal)) return FA_ERR_INVALID_ARG;
     if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARG;
-    if (table_stride < max_blocks || (long long)max_blocks * cache->page_size > 0x7fffffffLL - 4096)
+    if ((table_stride != 0 && table_stride < max_blocks) || (long long)max_blocks * cache->page_size > 0x7fffffffLL - 4096)
         return FA_ERR_INVALID_ARG;   // (keys of the last tile stay within 32 bits)
     if (q_stride < (long long)Hq * d || q_stride % 8 != 0) return FA_ERR_INVALID_ARG;
     if (R == 0 || T == 0) return FA_OK;

@@ -322,7 +322,7 @@ int rope(const void *q, long long q_stride, void *q_out, long long qo_stride, in
         return FA_ERR_INVALID_ARG;
     if (Hkv > 0 && (k == nullptr || k_out == nullptr || k_stride < (long long)Hkv * d || ko_stride < (long long)Hkv * d))
         return FA_ERR_INVALID_ARG;
-    if (positions == nullptr || pos_stride < T || Hq > 65535 || Hkv > 65535) return FA_ERR_INVALID_ARG;
+    if (positions == nullptr || (pos_stride != 0 && pos_stride < T) || Hq > 65535 || Hkv > 65535) return FA_ERR_INVALID_ARG;
     const size_t pos_b = (size_t(spec->num_axes - 1) * size_t(pos_stride) + size_t(T)) * 4;
     const Span in[] = {{q, rows_bytes(T, Hq, d, q_stride), 2}, {k, rows_bytes(T, Hkv, d, k_stride), 2}, {positions, pos_b, 4}};
     const Span out[] = {{q_out, rows_bytes(T, Hq, d, qo_stride), 2}, {k_out, rows_bytes(T, Hkv, d, ko_stride), 2}};
@@ -381,7 +381,7 @@ int rope_append(const void *q, long long q_stride, void *q_out, long long qo_str
     if (Hq > 0 && (q == nullptr || q_out == nullptr || q_stride < (long long)Hq * d || qo_stride < (long long)Hq * d))
         return FA_ERR_INVALID_ARG;
     if (k == nullptr || v == nullptr || k_stride < (long long)Hkv * d || v_stride < (long long)Hkv * d) return FA_ERR_INVALID_ARG;
-    if (slots == nullptr || positions == nullptr || pos_stride < T || Hq > 65535 || Hkv > 65535) return FA_ERR_INVALID_ARG;
+    if (slots == nullptr || positions == nullptr || (pos_stride != 0 && pos_stride < T) || Hq > 65535 || Hkv > 65535) return FA_ERR_INVALID_ARG;
     const size_t pos_b = (size_t(spec->num_axes - 1) * size_t(pos_stride) + size_t(T)) * 4;
     const size_t cache_b = cache_bytes(cache);
     if (cache_b > 0 && (cache->k == nullptr || cache->v == nullptr)) return FA_ERR_INVALID_ARG;

@@ -424,7 +424,7 @@ int fa_kv_release(const int *lens, const int *done, int R, const int *block_tabl
                   int max_blocks, int *free_blocks, const int *free_count, int num_blocks, int page_size,
                   int *lens_out, int *free_count_out, void *stream) {
     if (R < 0 || max_blocks < 0 || num_blocks < 0 || page_size < 1) return FA_ERR_INVALID_ARG;
-    if (table_stride < max_blocks) return FA_ERR_INVALID_ARG;
+    if (table_stride != 0 && table_stride < max_blocks) return FA_ERR_INVALID_ARG;   // 0: one row for all
     if (std::max({R, num_blocks}) > kMostItems) return FA_ERR_INVALID_ARG;
     if ((long long)max_blocks * page_size > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
     const size_t lens_b = size_t(R) * 4, tab_b = max_blocks > 0 ? table_bytes(R, table_stride, max_blocks) : 0;

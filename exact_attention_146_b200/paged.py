@@ -94,12 +94,16 @@ def _ints(name, t, n, dtype=None):
     return t.data_ptr()
 
 
-def _table(t, R):
-    """(pointer, entries from row to row, entries a row) of a block table."""
+def _table(t, R, written=False):
+    """(pointer, entries from row to row, entries a row) of a block table.  One that is only read may be a
+    single row for all requests (expanded: 0 entries from row to row); other rows may not overlap."""
     if t.dtype is _Types.i32 and t.is_cuda and t.dim() == 2:
         rows, width = t.shape
         if rows == R and (width <= 1 or t.stride(1) == 1):
-            return t.data_ptr(), (max(t.stride(0), width) if R > 1 else width), width
+            step = t.stride(0) if R > 1 else width
+            if step < width and (step != 0 or written):
+                raise ValueError(f"the rows of block_table overlap: {width} entries, {step} from row to row")
+            return t.data_ptr(), step, width
     raise ValueError(f"block_table must be an int32 CUDA tensor [{R}, max_blocks] with adjacent entries, got {t.dtype} {tuple(t.shape)}")
 
 
@@ -154,17 +158,20 @@ class RopeTable:
         self._axis = (ctypes.c_int * max(1, len(inv)))(*axes)
 
     def _spec(self, positions, T):
-        """(spec, pointer, elements from axis to axis) of positions [axes, T] or [T]."""
+        """(spec, pointer, elements from axis to axis) of positions [axes, T] or [T]; axes that share one row
+        (expanded) are 0 elements apart."""
         n, step = (positions.shape[0], positions.stride(0)) if positions.dim() == 2 else (1, T)
         if positions.dtype is not _Types.i32 or not positions.is_cuda or positions.dim() not in (1, 2) or \
                 positions.shape[-1] != T or (T > 1 and positions.stride(-1) != 1):
             raise ValueError(f"positions must be int32 CUDA [axes, {T}] (or [{T}]), got {positions.dtype} {tuple(positions.shape)}")
         if n < self.num_axes:
             raise ValueError(f"the table uses {self.num_axes} axes, positions has {n}")
+        if n > 1 and 0 != step < T:
+            raise ValueError(f"the axes of positions overlap: {T} tokens, {step} elements from axis to axis")
         spec = self._specs.get(n)
         if spec is None:
             spec = self._specs[n] = ctypes.byref(_RopeSpec(self.rot_dim, int(self.interleaved), n, self._inv, self._axis))
-        return spec, positions.data_ptr(), (max(step, T) if n > 1 else T)
+        return spec, positions.data_ptr(), (step if n > 1 else T)
 
 
 def fa_rope(q, positions, table: RopeTable, *, k=None, inverse: bool = False, q_out=None, k_out=None, stream=None):
@@ -248,7 +255,7 @@ def fa_kv_reserve(ctx_lens, new_lens, block_table, free_blocks, free_count, *, p
         slots = _empty((T,), _Types.i64, dev, stream)
     if free_count_out is None:
         free_count_out = _empty((1,), i32, dev, stream)
-    table, stride, width = _table(block_table, R)
+    table, stride, width = _table(block_table, R, written=True)
     blocks = free_blocks.numel()
     _run("fa_kv_reserve", stream, _ints("ctx_lens", ctx_lens, R), _ints("new_lens", new_lens, R), R, table, stride, width,
          _ints("free_blocks", free_blocks, blocks), _ints("free_count", free_count, 1), blocks, int(page_size), T,

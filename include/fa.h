@@ -297,8 +297,8 @@ int fa_merge_partials(const float *o_parts, const float *lse_parts, int R, void 
  *   pushed on the free stack in table order, requests in order (a block that two tables name is
  *   pushed by each: who shares blocks between requests counts their users); lens_out[r] = 0 for those and
  *   lens[r] for the others (lens_out may be lens, free_count_out may be free_count).  The table
- *   is not changed.  Lengths out of range, or more blocks than num_blocks in the stack: refused
- *   whole, as above.
+ *   is not changed, and table_stride may be 0: one row for all requests.  Lengths out of range, or more
+ *   blocks than num_blocks in the stack: refused whole, as above.
  * 0 <= R, T, num_blocks <= 2^30, max_blocks >= 0, page_size >= 1, max_blocks * page_size < 2^31.  int32 arrays
  * 4-byte aligned, slots 8-byte; empty arrays may be NULL.
  */
@@ -342,11 +342,11 @@ typedef struct fa_rope_spec {
 /*
  * fa_rope: q [T, Hq, d] -> q_out and k [T, Hkv, d] -> k_out, bf16 (fa_rope_f16: fp16), rows
  *   *_stride (>= heads * d) elements from token to token, so q, k may be slices of one fused
- *   projection; positions [num_axes, T] int32, axes pos_stride (>= T) apart.  inverse = 1 turns
- *   by the opposite angle: the gradient of the forward turn (dq, dk of the rotated rows -> of
- *   the rows).  Angles are formed in fp64 and applied in fp32, one rounding at the end.  Hq or
- *   Hkv may be 0.  In place (q_out == q with the same stride, k_out == k) is allowed; otherwise
- *   no output row may overlap an input row or another output row.
+ *   projection; positions [num_axes, T] int32, axes pos_stride (>= T, or 0: all axes have the
+ *   same positions) apart.  inverse = 1 turns by the opposite angle: the gradient of the forward
+ *   turn (dq, dk of the rotated rows -> of the rows).  Angles are formed in fp64 and applied in
+ *   fp32, one rounding at the end.  Hq or Hkv may be 0.  In place (q_out == q with the same stride,
+ *   k_out == k) is allowed; otherwise no output row may overlap an input row or another output row.
  * fa_rope_append: q as above (forward turn; q_out NULL with Hq = 0), and for each token t with
  *   slots[t] >= 0 the rotated k row and the v row go to slot slots[t] % page_size of block
  *   slots[t] / page_size of the cache.  Rows with a negative slot are left out: nothing
@@ -376,8 +376,8 @@ int fa_rope_append_f16(const void *q, long long q_stride, void *q_out, long long
  *   q   [T, Hq, d], rows q_stride (>= Hq * d, a multiple of 8) elements apart, 16-byte aligned:
  *       request r's new tokens are rows cu_seqlens[r] .. cu_seqlens[r + 1] - 1 (n_r of them)
  *   cache: keys and values (Hkv heads, Hq % Hkv == 0; query head h reads head h / (Hq / Hkv))
- *   block_table [R, max_blocks] (rows table_stride apart), cu_seqlens [R + 1], seq_lens [R]:
- *       int32 device arrays; seq_lens[r] = L_r keys in all, the new tokens' own among them
+ *   block_table [R, max_blocks] (rows table_stride >= max_blocks apart, or 0: one row for all),
+ *       cu_seqlens [R + 1], seq_lens [R]: int32 device arrays; seq_lens[r] = L_r keys in all, the new tokens' own among them
  *   out [T, Hq, d] dense, 16-byte aligned;  lse [Hq, T] fp32 natural log, or NULL
  *   max_new: an upper bound of n_r, known on the host;  max_blocks * page_size < 2^31 - 4096
  *

@@ -641,3 +641,48 @@ def test_captured_decoding_steps():
         torch.cuda.synchronize()
         assert torch.equal(bufs[1][1], eager_out[i][0]) and torch.equal(bufs[1][2], eager_out[i][1])
     assert graphed.seq_lens.tolist() == eager.seq_lens.tolist() == [p + 20 * o for p, o in zip(prompt, one.tolist())]
+
+
+# ------------------------------------------------------------------------------- shared rows
+
+@pytest.mark.parametrize("T", [1, 70, 3001])
+def test_positions_shared_by_all_axes(T):
+    """Text in a model of three axes: one row of positions, expanded.  Behind it lies something else."""
+    torch.manual_seed(T)
+    inv, axis = spec(64, 3)
+    table = fa.RopeTable(inv, axis=axis)
+    memory = torch.full((4 * T,), 77777, dtype=torch.int32, device="cuda")
+    memory[:T] = torch.arange(T, device="cuda") + 1000
+    shared = memory[:T][None].expand(3, T)
+    q, k, v = (torch.randn(T, h, 64, device="cuda").to(torch.bfloat16) for h in (4, 2, 2))
+    got = fa.fa_rope(q, shared, table, k=k)
+    for g, x in zip(got, (q, k)):
+        want = _paged.rope64(x, shared, inv, axis, False)
+        close(g, want, _paged.rope_tolerance(x, want, 32, False))
+    k_cache, v_cache, _ = _paged.make_paged([T], 16, 2, 64, torch.bfloat16, "nhd", 3, poison=False)
+    q_out = fa.fa_rope_append(q, k, v, shared, table, k_cache, v_cache, torch.arange(T, device="cuda"))
+    assert torch.equal(q_out, got[0]) and torch.equal(k_cache.reshape(-1, 2, 64)[:T], got[1])
+
+
+@pytest.mark.parametrize("new", [1, 90])
+def test_a_table_shared_by_all_requests(new):
+    """Samples of one prompt: one row of blocks, expanded; what only reads it takes it, what writes it does not."""
+    k, v, table = _paged.make_paged([200], 16, 2, 64, torch.bfloat16, "nhd", 5)
+    memory = torch.full((4, table.shape[1]), -3, dtype=torch.int32, device="cuda")
+    memory[0] = table[0]
+    shared = memory[:1].expand(3, -1)
+    lens, news = [200, 150, 200], [new, 1, new]
+    cu = [0, new, new + 1, 2 * new + 1]
+    q = torch.randn(cu[-1], 4, 64, device="cuda").to(torch.bfloat16)
+    out, lse = fa.fa_paged_fwd(q, k, v, shared, i32(cu), i32(lens), max_new=max(news))
+    want, z, t_out, t_lse = _paged.attend64(q, k, v, table.expand(3, -1), cu, lens, causal=True, window=None, scale=0.125)
+    close(out, want, t_out)
+    close(lse, z, t_lse)
+    stack = torch.full((40,), -9, dtype=torch.int32, device="cuda")
+    left, count = fa.fa_kv_release(i32([33, 20, 5]), i32([1, 0, 1]), shared, stack, i32([2]), page_size=16)
+    assert left.tolist() == [0, 20, 0] and count.tolist() == [6]
+    assert stack[2:6].tolist() == memory[0, :3].tolist() + memory[0, :1].tolist() and bool((stack[6:] == -9).all())
+    before = memory.clone()
+    with pytest.raises(ValueError, match="overlap"):
+        fa.fa_kv_reserve(i32([16, 16, 16]), i32([1, 1, 1]), shared, i32([0, 1, 2, 3]), i32([4]), page_size=16, num_tokens=3)
+    assert torch.equal(memory, before)

@@ -177,3 +177,46 @@ def test_binding_checks():
         fa.fa_kv_release(torch.zeros(2), torch.zeros(2), None, None, None, page_size=16)
     with pytest.raises(ValueError):
         fa.PagedKV(1, 1, 16, 1, 64, layout="dnh", device="cpu")
+
+
+class OnGpu:
+    """A CPU tensor that says it is on a GPU: for the binding's look at types, shapes and strides."""
+    is_cuda = True
+
+    def __init__(self, t):
+        self.t, self.dtype, self.shape = t, t.dtype, t.shape
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def test_expanded_positions_and_tables():
+    """The stride that the tensor has is the one that is passed on: 0 for one row that all axes (or
+    requests) share, and rows that overlap otherwise are refused."""
+    import torch
+    paged._init()
+    table = fa.RopeTable([1.0, 0.5, 0.25], axis=[0, 1, 2])
+    row = torch.arange(5, dtype=torch.int32)
+    assert table._spec(OnGpu(row[None].expand(3, 5)), 5)[1:] == (row.data_ptr(), 0)
+    assert table._spec(OnGpu(torch.zeros(3, 9, dtype=torch.int32)[:, :5]), 5)[2] == 9
+    assert table._spec(OnGpu(row[:1][None].expand(3, 1)), 1)[2] == 0
+    with pytest.raises(ValueError, match="overlap"):
+        table._spec(OnGpu(torch.as_strided(torch.arange(16, dtype=torch.int32), (3, 5), (4, 1))), 5)
+    blocks = torch.arange(8, dtype=torch.int32)
+    shared = OnGpu(blocks[None].expand(4, 8))
+    assert paged._table(shared, 4) == (blocks.data_ptr(), 0, 8)
+    with pytest.raises(ValueError, match="overlap"):
+        paged._table(shared, 4, written=True)
+    for written in (False, True):
+        with pytest.raises(ValueError, match="overlap"):
+            paged._table(OnGpu(torch.as_strided(torch.arange(40, dtype=torch.int32), (4, 8), (7, 1))), 4, written)
+        assert paged._table(OnGpu(torch.zeros(4, 12, dtype=torch.int32)[:, :8]), 4, written)[1:] == (12, 8)
+        assert paged._table(OnGpu(blocks[None]), 1, written)[1:] == (8, 8)
+
+
+def test_one_row_for_all(L):
+    """A stride of 0 from axis to axis or row to row, where the array is only read."""
+    assert rope(L, ps=0, s=spec(axes=3)) in NO_DEVICE and append(L, ps=0, s=spec(axes=3)) in NO_DEVICE
+    assert attend(L, stride=0) in NO_DEVICE and release(L, stride=0) in NO_DEVICE
+    assert reserve(L, stride=0) == fa.FA_ERR_INVALID_ARG
+    assert rope(L, ps=-7) == attend(L, stride=-8) == release(L, stride=-8) == fa.FA_ERR_INVALID_ARG
