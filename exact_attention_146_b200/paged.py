@@ -327,6 +327,8 @@ def fa_paged_fwd(q, k_cache, v_cache, block_table, cu_seqlens, seq_lens, *, max_
         raise ValueError(f"window must be at least 1, got {window}")
     if workspace is None:
         workspace = _empty((max(1, paged_workspace_bytes(Hq, c.Hkv, d)),), _Types.torch.uint8, q.device, stream)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor, got strides {workspace.stride()} on {workspace.device}")
     _run("fa_paged_fwd" + f16, stream, qp, qs, ctypes.byref(c), table, stride, width, _ints("cu_seqlens", cu_seqlens, R + 1),
          _ints("seq_lens", seq_lens, R), R, T, Hq, int(max_new), d ** -0.5 if scale is None else float(scale), 1 if causal else 0,
          int(window), out.data_ptr(), lse_p, workspace.data_ptr(), workspace.numel() * workspace.element_size())

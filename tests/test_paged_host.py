@@ -220,3 +220,20 @@ def test_one_row_for_all(L):
     assert attend(L, stride=0) in NO_DEVICE and release(L, stride=0) in NO_DEVICE
     assert reserve(L, stride=0) == fa.FA_ERR_INVALID_ARG
     assert rope(L, ps=-7) == attend(L, stride=-8) == release(L, stride=-8) == fa.FA_ERR_INVALID_ARG
+
+
+def test_a_workspace_has_the_bytes_that_it_counts():
+    """numel() of an expanded or strided tensor says more than there is memory behind its pointer, or skips some."""
+    import torch
+    paged._init()
+    q, out = (OnGpu(torch.zeros(2, 4, 64, dtype=torch.bfloat16)) for _ in range(2))
+    cache = OnGpu(torch.zeros(3, 16, 2, 64, dtype=torch.bfloat16))
+    ints = [OnGpu(torch.zeros(n, dtype=torch.int32)) for n in (2, 1)]
+    table = OnGpu(torch.zeros(1, 3, dtype=torch.int32))
+    need = fa.paged_workspace_bytes(4, 2, 64)
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(need), torch.zeros(2 * need, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            fa.fa_paged_fwd(q, cache, cache, table, *ints, max_new=2, out=out, return_lse=False, workspace=OnGpu(ws), stream=0)
+    with pytest.raises(ValueError, match="workspace"):
+        fa.fa_paged_fwd(q, cache, cache, table, *ints, max_new=2, out=out, return_lse=False, workspace=torch.zeros(need, dtype=torch.uint8),
+                        stream=0)
