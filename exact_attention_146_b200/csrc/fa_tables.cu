@@ -37,6 +37,11 @@ constexpr int kMostItems = 1 << 30;   // requests, tokens, blocks: strided loops
 // Tokens up to which one cluster does a step.
 constexpr int kClusterTokens = 16384;
 constexpr int kBatch = 4;   // tokens or blocks a thread has in flight
+// Tokens and blocks of a chunk of kTableThreads requests are summed in the halves of one 64-bit word.  A
+// request has at most T new tokens and no more new blocks than tokens, so neither half carries while T
+// is below this; from here on the totals are summed apart before the halves are relied on.
+constexpr int kPackedTokens = 1 << 22;
+static_assert((long long)kTableThreads * (kPackedTokens - 1) < 1LL << 32, "a chunk's tokens fit 32 bits");
 
 __device__ __forceinline__ int blocks_of(int tokens, int page) {   // tokens + page - 1 may pass 2^31
     return int((unsigned(tokens) + unsigned(page) - 1u) / unsigned(page));
@@ -53,9 +58,8 @@ __device__ __forceinline__ unsigned long long warp_scan(unsigned long long x) {
     return x;
 }
 
-// Inclusive scan over the block of a pair of sums packed in 64 bits (low: tokens, high: blocks;
-// each below 2^31, so the halves never carry).  `warp_sums`: 32 words of shared memory; `flag` becomes
-// its OR over the block.
+// Inclusive scan over the block.  `warp_sums`: 32 words of shared memory; `flag` becomes its OR over the
+// block.
 __device__ __forceinline__ unsigned long long block_scan(unsigned long long x, unsigned long long *warp_sums,
                                                          unsigned long long *total, int &flag) {
     const int lane = int(threadIdx.x) % 32, warp = int(threadIdx.x) / 32, warps = int(blockDim.x) / 32;
@@ -109,9 +113,9 @@ __global__ void __launch_bounds__(kTableThreads) fa_kv_reserve_kernel(const __gr
     const int tid = int(threadIdx.x), nt = int(blockDim.x);
     const int count = *p.free_count;
 
-    // Totals, and whether every length fits: a step that does not fit is refused whole.  (Sums that
-    // leave 31 bits are caught by the running check: no step has that many tokens or blocks.)
+    // Totals, and whether every length fits: a step that does not fit is refused whole.
     long long tokens = 0, blocks = 0;
+    unsigned long long my_tokens = 0, my_blocks = 0;   // this thread's requests
     int bad = 0;
     int ctx0 = 0, new0 = 0;   // this thread's request of the first chunk
     unsigned long long upto0 = 0, total0 = 0;
@@ -125,7 +129,10 @@ __global__ void __launch_bounds__(kTableThreads) fa_kv_reserve_kernel(const __gr
             if (rank == 0 && PART != ReservePart::Lengths)
                 report_range(p.status, n > p.T && c >= 0 ? kSiteTokens : kSiteLengths, r);
         } else {
-            mine = (unsigned long long)(unsigned)n | ((unsigned long long)(unsigned)(blocks_of(c + n, p.page) - blocks_of(c, p.page)) << 32);
+            const unsigned need = unsigned(blocks_of(c + n, p.page) - blocks_of(c, p.page));
+            mine = (unsigned long long)(unsigned)n | ((unsigned long long)need << 32);
+            my_tokens += unsigned(n);
+            my_blocks += need;
         }
         unsigned long long total = 0;
         const unsigned long long upto = block_scan(mine, warp_sums, &total, off);
@@ -133,6 +140,14 @@ __global__ void __launch_bounds__(kTableThreads) fa_kv_reserve_kernel(const __gr
         tokens += (long long)(total & 0xffffffffu);
         blocks += (long long)(total >> 32);
         if (base == 0) ctx0 = c, new0 = n, upto0 = upto - mine, total0 = total;
+    }
+    if (p.T >= kPackedTokens) {   // (a step that passes has at most 2^30 of each, and its packed sums are right)
+        unsigned long long all = 0;
+        int none = 0;
+        block_scan(my_tokens, warp_sums, &all, none);
+        tokens = (long long)all;
+        block_scan(my_blocks, warp_sums, &all, none);
+        blocks = (long long)all;
     }
     if (!bad && tokens > p.T) {
         bad = 1;

@@ -686,3 +686,67 @@ def test_a_table_shared_by_all_requests(new):
     with pytest.raises(ValueError, match="overlap"):
         fa.fa_kv_reserve(i32([16, 16, 16]), i32([1, 1, 1]), shared, i32([0, 1, 2, 3]), i32([4]), page_size=16, num_tokens=3)
     assert torch.equal(memory, before)
+
+
+# ------------------------------------------------------------------------------- steps of many tokens
+
+def refused(ctx, new, table, stack, count, site, T, page, in_place):
+    """The step is refused whole: reported, and nothing is taken."""
+    before, ctx_d, count_d = table.clone(), i32(ctx), i32([count])
+    kw = dict(seq_lens=ctx_d, free_count_out=count_d) if in_place else {}
+    cu, lens, pos, slots, cnt = fa.fa_kv_reserve(ctx_d, i32(new), table, stack, count_d, page_size=page, num_tokens=T, **kw)
+    st, word = fa.device_status()
+    assert st == fa.FA_ERR_PAGED_RANGE and (word >> 8) & 0xFF == site
+    assert not bool(cu.any()) and lens.tolist() == ctx and cnt.tolist() == [count]
+    assert bool((slots == -1).all()) and not bool(pos.any()) and torch.equal(table, before)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("ctx,new,count,site", [
+    ([3, -1], [9000, 9000], 6000, 41), ([3, 20], [15000, -2], 6000, 41), ([3, 39990], [9000, 9000], 6000, 41),
+    ([3, 20], [15000, 10000], 6000, 42), ([3, 20], [30000, 1], 6000, 42),
+    ([0, 0], [9000, 9000], 1000, 43), ([0, 0], [9000, 9000], 6001, 43), ([0, 0], [9000, 9000], -1, 43)])
+def test_reserve_of_many_tokens_refuses_a_whole_step(ctx, new, count, site, in_place):
+    table = torch.full((2, 2500), 7, dtype=torch.int32, device="cuda")
+    refused(ctx, new, table, torch.arange(6000, dtype=torch.int32, device="cuda"), count, site, 20000, 16, in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("R,ctx,new", [(1024, 0, 1 << 22), (1024, 5, 1 << 22), (1024, 0, (1 << 22) + 1), (2048, 0, 1 << 22), (512, 0, 1 << 23),
+                                       (1025, 0, 1 << 22)])
+def test_reserve_refuses_sums_beyond_32_bits(R, ctx, new, in_place):
+    """The new tokens of many requests sum to a multiple of 2^32, or a little more: not a step of few tokens."""
+    table = torch.full((R, 3), 7, dtype=torch.int32, device="cuda")
+    refused([ctx] * R, [new] * R, table, torch.arange(8192, dtype=torch.int32, device="cuda"), 8192, 42, new, 1 << 22, in_place)
+
+
+def test_reserve_of_millions_of_tokens():
+    """A step large enough for the sums to be made apart, that fits: against the formulas on the GPU."""
+    page, ctx, new = 128, [1000, 0, 77, 2_000_000], [1 << 21, 0, 5, (1 << 21) + 300]
+    T = sum(new) + 9
+    held, want = ([_paged.blocks_of(x, page) for x in xs] for xs in (ctx, [c + n for c, n in zip(ctx, new)]))
+    width = max(want)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    ids = torch.randperm(sum(want) + 3, device="cuda", generator=g).int()
+    table = torch.full((4, width), -7, dtype=torch.int32, device="cuda")
+    at = 0
+    for r in range(4):
+        table[r, :held[r]] = ids[at:at + held[r]]
+        at += held[r]
+    stack, count = torch.cat([ids[at:], torch.full((at,), -9, dtype=torch.int32, device="cuda")]), ids.numel() - at
+    ref = table.clone()
+    top = count
+    for r in range(4):
+        n = want[r] - held[r]
+        ref[r, held[r]:want[r]] = stack[top - n:top].flip(0)
+        top -= n
+    cu, lens, pos, slots, cnt = fa.fa_kv_reserve(i32(ctx), i32(new), table, stack, i32([count]), page_size=page, num_tokens=T)
+    assert torch.equal(table, ref) and cnt.tolist() == [top] and lens.tolist() == [c + n for c, n in zip(ctx, new)]
+    starts = [sum(new[:r]) for r in range(5)]
+    assert cu.tolist() == starts
+    for r in range(4):
+        x = torch.arange(ctx[r], ctx[r] + new[r], device="cuda")
+        assert torch.equal(pos[starts[r]:starts[r + 1]].long(), x)
+        assert torch.equal(slots[starts[r]:starts[r + 1]], ref[r].long()[x // page] * page + x % page)
+    assert bool((slots[starts[4]:] == -1).all()) and not bool(pos[starts[4]:].any())
