@@ -156,8 +156,9 @@ __device__ void paged_plan_role(const PagedTileParams &p, int seg, int whole_uni
                 const int t0 = t * p.tq, t1 = min(w.tokens, t0 + p.tq);
                 if (t0 >= t1) continue;
                 const int last = p.plan.causal ? w.pos0 + t1 - 1 : w.L - 1;
-                const int from = p.plan.window > 0 ? w.pos0 + t0 - p.plan.window + 1 : 0;
-                const int js = max(max(from, 0) / C::BC, piece.js), je = min(max(last, 0) / C::BC + 1, piece.je);
+                // in 64 bits: a position below 0 (more new tokens than keys) less a window near 2^31
+                const long long from = p.plan.window > 0 ? (long long)w.pos0 + t0 - p.plan.window + 1 : 0;
+                const int js = max(int(max(from, 0LL)) / C::BC, piece.js), je = min(max(last, 0) / C::BC + 1, piece.je);
                 if (je <= js) continue;
                 w.js[t] = js;
                 w.je[t] = je;
@@ -272,8 +273,9 @@ __device__ void paged_softmax_role(const PagedTileParams &p, PagedUnits<C, kRole
         const int token = t * p.tq + i_tok;            // of the unit
         const int at0 = w.pos0 + t * p.tq, at = at0 + i_tok;   // positions: the row tile's first token, this row's
         const bool window = p.plan.window > 0;
-        const RowKeys keys{w.L, p.plan.causal ? at : 0x7fffffff, window ? at - p.plan.window + 1 : -0x7fffffff,
-                           p.plan.causal ? at0 : 0x7fffffff, window ? at0 + p.tq - p.plan.window : -0x7fffffff};
+        // (rows before the first key see none: their lower bound does not matter, and -1 keeps it within 32 bits)
+        const RowKeys keys{w.L, p.plan.causal ? at : 0x7fffffff, window ? max(at, -1) - p.plan.window + 1 : -0x7fffffff,
+                           p.plan.causal ? at0 : 0x7fffffff, window ? max(at0 + p.tq - 1, -1) - p.plan.window + 1 : -0x7fffffff};
         float m_ref = -INFINITY, l = 0.f;
         if (!softmax_tiles<C>(sbase, tmem, ctl, t, quarter, p.scale_log2, keys, js, je, scnt, ocnt, m_ref, l)) goto unwind;
         if (nk > 0) {

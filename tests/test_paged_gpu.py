@@ -750,3 +750,13 @@ def test_reserve_of_millions_of_tokens():
         assert torch.equal(pos[starts[r]:starts[r + 1]].long(), x)
         assert torch.equal(slots[starts[r]:starts[r + 1]], ref[r].long()[x // page] * page + x % page)
     assert bool((slots[starts[4]:] == -1).all()) and not bool(pos[starts[4]:].any())
+
+
+# ------------------------------------------------------------------------------- windows without a limit
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 200, 1 << 30, 400])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_window_of_any_size_over_fewer_keys_than_tokens(d, window):
+    """Positions below 0 less a window near 2^31: rows that see keys keep them."""
+    attend([100, 300, 0, 7], [300, 300, 200, 20], Hq=4, Hkv=2, d=d, page=16, window=window, seed=d)
+    attend([3, 300, 0, 1], [5, 1, 2, 1], Hq=4, Hkv=2, d=d, page=16, window=window, seed=d)
