@@ -367,21 +367,35 @@ class PagedKV:
         self.free_count = torch.full((1,), num_blocks, **ints)
         self.cu_seqlens = torch.zeros(max_requests + 1, **ints)
         self.positions = self.slots = None
-        self._rows = {}   # num_tokens -> (positions, slots): kept, so that a captured step's buffers stay its own
+        self._buffers = {}    # rows, a power of two -> (positions, slots)
+        self._last = (None, None)
 
-    def reserve(self, new_lens, num_tokens: int, *, stream=None):
+    def _rows_of(self, num_tokens: int, stream):
+        """Positions and slots of a step of num_tokens rows: the start of buffers of the next power of two.  They are
+        kept, and a number of rows has always the same ones, as a captured step expects; all of them together
+        have about four times the most rows at most."""
+        if self._last[0] is None or self._last[0].shape[0] != num_tokens:
+            size = max(64, 1 << max(0, num_tokens - 1).bit_length())
+            if size not in self._buffers:
+                self._buffers[size] = tuple(_empty((size,), t, self.seq_lens.device, stream) for t in (_Types.i32, _Types.i64))
+            self._last = tuple(b[:num_tokens] for b in self._buffers[size])
+        return self._last
+
+    def reserve(self, new_lens, num_tokens: int, *, positions=None, slots=None, stream=None):
         """Room for new_lens [max_requests] int32 more tokens, num_tokens rows in all (rows behind the last
-        token are allowed: a captured step of fixed size).  Returns positions and slots."""
+        token are allowed: a captured step of fixed size).  Returns positions and slots: those given
+        ([num_tokens] int32 and int64), or buffers of this cache, which the next reserve may fill anew."""
         if self.tables is not self:
             raise ValueError("reserve on the layer that holds the tables")
-        if num_tokens not in self._rows:
-            self._rows[num_tokens] = (_empty((num_tokens,), _Types.i32, self.seq_lens.device, stream),
-                                      _empty((num_tokens,), _Types.i64, self.seq_lens.device, stream))
-        self.positions, self.slots = self._rows[num_tokens]
+        num_tokens = int(num_tokens)
+        if positions is None or slots is None:
+            kept = self._rows_of(num_tokens, stream)
+            positions, slots = kept[0] if positions is None else positions, kept[1] if slots is None else slots
         fa_kv_reserve(self.seq_lens, new_lens, self.block_table, self.free_blocks, self.free_count, page_size=self.page_size,
-                      cu_seqlens=self.cu_seqlens, seq_lens=self.seq_lens, positions=self.positions, slots=self.slots,
+                      num_tokens=num_tokens, cu_seqlens=self.cu_seqlens, seq_lens=self.seq_lens, positions=positions, slots=slots,
                       free_count_out=self.free_count, stream=stream)
-        return self.positions, self.slots
+        self.positions, self.slots = positions, slots
+        return positions, slots
 
     def append(self, q, k, v, table: RopeTable, *, positions=None, q_out=None, stream=None):
         """Rotates q and k by `positions` (default: the positions in the requests) and stores k and v."""

@@ -760,3 +760,48 @@ def test_window_of_any_size_over_fewer_keys_than_tokens(d, window):
     """Positions below 0 less a window near 2^31: rows that see keys keep them."""
     attend([100, 300, 0, 7], [300, 300, 200, 20], Hq=4, Hkv=2, d=d, page=16, window=window, seed=d)
     attend([3, 300, 0, 1], [5, 1, 2, 1], Hq=4, Hkv=2, d=d, page=16, window=window, seed=d)
+
+
+# ------------------------------------------------------------------------------- a step's rows
+
+def test_rows_of_steps_kept_by_the_caller():
+    """Two steps of different sizes, the first one's rows given: they outlive the second step; rows of the cache
+    itself, captured with append and attend behind an eager reserve, stay where they are."""
+    torch.manual_seed(21)
+    table = fa.RopeTable(spec(64, 1)[0])
+    kv = fa.PagedKV(2, 64, 16, 2, 64, max_blocks=32)
+    mine = torch.full((70,), -5, dtype=torch.int32, device="cuda"), torch.full((70,), -5, dtype=torch.int64, device="cuda")
+    got = kv.reserve(i32([40, 30]), 70, positions=mine[0], slots=mine[1])
+    assert got[0] is mine[0] and got[1] is mine[1]
+    kept = mine[1].clone()
+    q, k, v = (torch.randn(70, h, 64, device="cuda").to(torch.bfloat16) for h in (4, 2, 2))
+    kv.append(None, k, v, table)
+    kv.reserve(i32([1, 1]), 5)
+    assert torch.equal(mine[1], kept) and mine[0].tolist() == list(range(40)) + list(range(30))
+    q5, k5, v5 = (torch.randn(5, h, 64, device="cuda").to(torch.bfloat16) for h in (4, 2, 2))
+    out, q_rot = torch.zeros_like(q5), torch.zeros_like(q5)
+    ws = torch.empty(fa.paged_workspace_bytes(4, 2, 64), dtype=torch.uint8, device="cuda")
+
+    def rest():
+        kv.append(q5, k5, v5, table, q_out=q_rot)
+        kv.attend(q_rot, max_new=1, out=out, return_lse=False, workspace=ws)
+    rest()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        rest()
+    for n in (1, 300, 9, 64):   # steps of other sizes, with no tokens, between
+        kv.reserve(i32([0, 0]), n)
+    for x in (q5, k5, v5):
+        x.normal_()
+    kv.reserve(i32([1, 1]), 5)
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    got = out.clone()
+    lens = kv.seq_lens.tolist()
+    assert lens == [42, 32]
+    want, _, t_out, _ = _paged.attend64(q_rot, kv.k_cache, kv.v_cache, kv.block_table, [0, 1, 2], lens, causal=True, window=None, scale=0.125)
+    close(got[:2], want[:2], t_out[:2])
+    at = kv.slots[:2]
+    assert torch.equal(kv.v_cache.reshape(-1, 2, 64)[at], v5[:2])

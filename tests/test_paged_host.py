@@ -237,3 +237,37 @@ def test_a_workspace_has_the_bytes_that_it_counts():
     with pytest.raises(ValueError, match="workspace"):
         fa.fa_paged_fwd(q, cache, cache, table, *ints, max_new=2, out=out, return_lse=False, workspace=torch.zeros(need, dtype=torch.uint8),
                         stream=0)
+
+
+def test_a_cache_keeps_few_buffers(monkeypatch):
+    """Steps of every size: what is kept grows with the largest step, not with the number of sizes, and a size
+    has the same buffers each time."""
+    import torch
+    steps = []
+    monkeypatch.setattr(paged, "fa_kv_reserve", lambda *a, **kw: steps.append((kw["num_tokens"], kw["positions"], kw["slots"])))
+    kv = fa.PagedKV(2, 4, 16, 1, 64, device="cpu")
+    at = {}
+    for n in list(range(0, 3000)) + [7, 2999, 64, 65, 1]:
+        pos, slots = kv.reserve(None, n)
+        assert steps[-1] == (n, pos, slots) and kv.positions is pos and kv.slots is slots
+        assert pos.shape == slots.shape == (n,) and pos.dtype == torch.int32 and slots.dtype == torch.int64
+        assert n == 0 or at.setdefault(n, (pos.data_ptr(), slots.data_ptr())) == (pos.data_ptr(), slots.data_ptr())
+    kept = sum(t.numel() for pair in kv._buffers.values() for t in pair)
+    assert kept <= 2 * 4 * 2999
+    mine = torch.zeros(5, dtype=torch.int32), torch.zeros(5, dtype=torch.int64)
+    kept = dict(kv._buffers)
+    assert kv.reserve(None, 5, positions=mine[0], slots=mine[1]) == mine and kv.positions is mine[0] and kv.slots is mine[1]
+    pos, slots = kv.reserve(None, 5, slots=mine[1])
+    assert slots is mine[1] and pos.data_ptr() == at[5][0] and kv._buffers == kept
+    assert kv.reserve(None, 5)[1].data_ptr() == at[5][1]
+
+
+def test_given_rows_of_the_wrong_size():
+    import torch
+    kv = fa.PagedKV(2, 4, 16, 1, 64, device="cpu")
+    for name in ("seq_lens", "block_table", "free_blocks", "free_count", "cu_seqlens"):
+        setattr(kv, name, OnGpu(getattr(kv, name)))
+    rows = dict(positions=OnGpu(torch.zeros(6, dtype=torch.int32)), slots=OnGpu(torch.zeros(5, dtype=torch.int64)))
+    with pytest.raises(ValueError, match="positions"):
+        kv.reserve(OnGpu(torch.zeros(2, dtype=torch.int32)), 5, stream=0, **rows)
+    assert kv.slots is None
