@@ -21,7 +21,9 @@
 // type; the error is half a step of each weight, and l sums the unrounded values), O once at the end.
 //
 // At the end of a unit the warp writes O / l and LSE, or, where a cut of the line crosses the unit, its
-// own normalised O and LSE to the workspace (fp32); the merge kernel combines those in the order of the workers:  LSE = ln sum_s e^LSE_s,  O = sum_s e^(LSE_s - LSE) O_s.
+// own normalised O and LSE to the workspace (fp32); the merge kernel combines those in the order of
+// the workers:  LSE = ln sum_s e^LSE_s,  O = sum_s e^(LSE_s - LSE) O_s.  A row whose sum is NaN has LSE = NaN in its
+// pieces too, so that it comes out NaN wherever the cuts fall.
 //
 // Measured (B200, in a CUDA graph): 48 requests of 4k to 16k keys (Hq 32, Hkv 8, d 128) 247 us, 6.56 TB/s (the measured copy
 // rate is 6.55); 4 requests of up to 1000 keys 11.6 us: the plan 4, the first copies 2, the merge 3.
@@ -535,8 +537,8 @@ fa_paged_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
                     float sum = l[r][c];
 #pragma unroll
                     for (int x = 4; x < 32; x *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-                    inv[c] = sum > 0.f ? 1.f / sum : 0.f;
-                    lse[c] = sum > 0.f ? (m[r][c] + log2f(sum)) * kLn2 : -INFINITY;
+                    inv[c] = sum == 0.f ? 0.f : 1.f / sum;   // (a sum that is NaN stays NaN, in both)
+                    lse[c] = sum == 0.f ? -INFINITY : (m[r][c] + log2f(sum)) * kLn2;
                 }
                 if (whole) {   // transposed back: row g, d 2 (lane % 4), + 1
                     const int row = 8 * r + g, i = row / p.pack;
@@ -622,7 +624,7 @@ __device__ __forceinline__ void merge_unit(const PagedParams &p, const MergeJob 
 #pragma unroll
             for (int o = 4; o > 0; o /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             const float now = fmaxf(m, __shfl_sync(0xffffffffu, mx, 0));
-            if (now == -INFINITY) continue;
+            if (now == -INFINITY && !__any_sync(0xffffffffu, isnan(ls))) continue;   // (a NaN makes all weights NaN, and the row)
             const float wl = __expf(ls - now), keep = __expf(m - now);
             m = now;
             sum *= keep;
@@ -670,7 +672,7 @@ __device__ __forceinline__ void merge_unit(const PagedParams &p, const MergeJob 
             m = all;
         }
         if (!real || helper != 0) continue;
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const long long at = job.row0 + token;
 #pragma unroll
         for (int e = 0; e < PER; ++e) {
@@ -686,7 +688,7 @@ __device__ __forceinline__ void merge_unit(const PagedParams &p, const MergeJob 
                     *reinterpret_cast<uint32_t *>(dst + v) = sm100::pack_x2<F16>(acc[e][v] * inv, acc[e][v + 1] * inv);
             }
         }
-        if (p.lse != nullptr && lane == 0) p.lse[(long long)head * p.plan.T + at] = sum > 0.f ? m + logf(sum) : -INFINITY;
+        if (p.lse != nullptr && lane == 0) p.lse[(long long)head * p.plan.T + at] = sum == 0.f ? -INFINITY : m + logf(sum);
     }
 }
 

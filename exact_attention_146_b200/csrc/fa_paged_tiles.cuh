@@ -285,8 +285,8 @@ __device__ void paged_softmax_role(const PagedTileParams &p, PagedUnits<C, kRole
         }
         ocnt += uint32_t(nk);
         {
-            const float inv_l = l > 0.f ? 1.f / l : 0.f;
-            const float lse = l > 0.f ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
+            const float inv_l = l == 0.f ? 0.f : 1.f / l;   // (a sum that is NaN stays NaN, in both)
+            const float lse = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
             const bool store = i_tok < p.tq && token < w.tokens;
             const bool whole = w.slot < 0;
             const long long row = w.row0 + token;

@@ -805,3 +805,37 @@ def test_rows_of_steps_kept_by_the_caller():
     close(got[:2], want[:2], t_out[:2])
     at = kv.slots[:2]
     assert torch.equal(kv.v_cache.reshape(-1, 2, 64)[at], v5[:2])
+
+
+# ------------------------------------------------------------------------------- NaN
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lens,news,bad", [
+    ([9000], [1], [0]), ([9000], [3], [1]), ([9000, 40], [2, 1], [1, 2]), ([40, 17], [1, 1], [1]),    # few rows, cut or whole
+    ([9000], [200], [0, 100, 199]), ([9000, 300, 20], [150, 130, 1], [3, 149, 170, 280]), ([40, 60], [40, 60], [5, 41])])
+def test_a_row_of_nan_stays_nan(lens, news, bad, d):
+    """q of NaN: O and LSE are NaN in that row, whether or not its unit is cut into pieces; the others are right."""
+    k, v, table = _paged.make_paged(lens, 16, 2, d, torch.bfloat16, "nhd", d)
+    cu = [0]
+    for n in news:
+        cu.append(cu[-1] + n)
+    q = torch.randn(cu[-1], 8, d, device="cuda").to(torch.bfloat16)
+    clean = q.clone()
+    q[bad] = float("nan")
+    out, lse = fa.fa_paged_fwd(q, k, v, table, i32(cu), i32(lens), max_new=max(news))
+    assert bool(out[bad].isnan().all()) and bool(lse[:, bad].isnan().all())
+    rest = [t for t in range(cu[-1]) if t not in bad]
+    want, z, t_out, t_lse = _paged.attend64(clean, k, v, table, cu, lens, causal=True, window=None, scale=d ** -0.5)
+    close(out[rest], want[rest], t_out[rest])
+    close(lse[:, rest], z[:, rest], t_lse[:, rest])
+
+
+@pytest.mark.parametrize("new", [1, 200])
+def test_one_nan_key_is_not_lost(new):
+    """A key of NaN in the middle of a long request: every row that sees it is NaN (d = 128: each weight is an exponential)."""
+    k, v, table = _paged.make_paged([9000], 16, 2, 128, torch.bfloat16, "nhd", 1)
+    k[table[0, 100].item(), 3, 0] = float("nan")
+    q = torch.randn(new, 8, 128, device="cuda").to(torch.bfloat16)
+    out, lse = fa.fa_paged_fwd(q, k, v, table, i32([0, new]), i32([9000]), max_new=new)
+    assert bool(out[:, :4].isnan().all()) and bool(lse[:4].isnan().all())
+    assert not bool(out[:, 4:].isnan().any()) and not bool(lse[4:].isnan().any())
