@@ -839,3 +839,72 @@ def test_one_nan_key_is_not_lost(new):
     out, lse = fa.fa_paged_fwd(q, k, v, table, i32([0, new]), i32([9000]), max_new=new)
     assert bool(out[:, :4].isnan().all()) and bool(lse[:4].isnan().all())
     assert not bool(out[:, 4:].isnan().any()) and not bool(lse[4:].isnan().any())
+
+
+# ------------------------------------------------------------------------------- every key once
+
+def counted(lens, news, *, Hq, Hkv, d, page, dtype, window=None, max_new=None):
+    """q = 0: every visible key has the weight 1, so LSE = ln(visible keys), and with V one-hot (the column
+    turns with every 8 keys and every head) O counts the keys of each column: a key left out, or taken
+    twice, shows in a request of tens of thousands.
+
+    Tolerances.  exp2(0) is 1 (its polynomial form, in the tile kernel at d = 32 and 64, is off by up to 2^-13.5),
+    and sums of ones are exact.  A piece's LSE: log2f (1 ulp), two products with rounded factors, four steps
+    of 2^-23 ln(keys) in all with the final sum m + logf.  The weights of up to `parts` pieces: __expf of
+    an argument of at most 8 (12 ulp) of those LSEs, 2^-19 in all; their sum adds 2^-24 each.  A unit has no more
+    pieces than CTAs of the tile kernel (148) or sqrt(8 steps) + 2 of the few-rows kernel, steps of 16
+    keys at least.  O is rounded once more to its type."""
+    k, v, table = _paged.make_paged(lens, page, Hkv, d, dtype, "nhd", 31)
+    cu = [0]
+    for n in news:
+        cu.append(cu[-1] + n)
+    head = torch.arange(Hkv, device="cuda")
+    want = torch.zeros(cu[-1], Hq, d, dtype=torch.float64, device="cuda")
+    z = torch.zeros(Hq, cu[-1], dtype=torch.float64, device="cuda")
+    seen = torch.ones(cu[-1], dtype=torch.float64, device="cuda")
+    for r, L in enumerate(lens):
+        j = torch.arange(L, device="cuda")
+        hot = torch.nn.functional.one_hot((j[:, None] // 8 + 5 * head) % d, d)
+        v[table[r].long()[j // page], j % page] = hot.to(dtype)
+        upto = torch.cat([torch.zeros_like(hot[:1]), hot.cumsum(0)])              # [L + 1, Hkv, d]
+        last = torch.arange(L - news[r], L, device="cuda")
+        first = (last - window + 1).clamp(min=0) if window else torch.zeros_like(last)
+        n = (last - first + 1).double()
+        rows = slice(cu[r], cu[r + 1])
+        want[rows] = ((upto[last + 1] - upto[first]).double() / n[:, None, None]).repeat_interleave(Hq // Hkv, 1)
+        z[:, rows] = n.log()
+        seen[rows] = n
+    polynomial = 2.0 ** -13.5 if d in (32, 64) and (max(news) if max_new is None else max_new) * (Hq // Hkv) > 16 else 0.0
+    parts = max(148, math.sqrt(8 * max(lens) / 16) + 2)
+    rel = polynomial + 2.0 ** -19 + parts * 2.0 ** -24
+    t_lse = rel + 4 * 2.0 ** -23 * z.abs()
+    assert bool((t_lse < torch.log(seen / (seen - 1).clamp(min=0.5))).all())      # a key more or less is outside
+    q = torch.zeros(cu[-1], Hq, d, device="cuda", dtype=dtype)
+    out, lse = fa.fa_paged_fwd(q, k, v, table, i32(cu), i32(lens), max_new=max(news) if max_new is None else max_new, window=window)
+    close(lse, z, t_lse)
+    close(out, want, (_paged.HALF[dtype] + 2 * rel + 2.0 ** -21) * want + 2.0 ** -25)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("lens,news,Hq,Hkv,d,page", [
+    ([40000], [1], 8, 1, 128, 64), ([40000], [1], 8, 8, 64, 16), ([30000], [3], 8, 2, 256, 16), ([40000], [1], 12, 1, 128, 16),
+    ([20000, 9000, 300, 1], [1, 1, 1, 1], 16, 4, 128, 16), ([25000, 70], [2, 2], 4, 2, 80, 100), ([40000], [1], 4, 1, 32, 3),
+    ([30000], [200], 8, 1, 128, 64), ([20000], [130], 4, 4, 192, 16), ([9000, 40, 5000], [700, 1, 90], 8, 2, 128, 16),
+    ([30000], [300], 4, 1, 256, 24), ([4000, 600], [140, 600], 4, 2, 64, 16), ([3000], [200], 3, 1, 32, 8),
+    ([10000, 17], [40, 17], 6, 2, 96, 32), ([12000], [700], 2, 2, 80, 100), ([20000], [20], 40, 1, 128, 16)])
+def test_every_key_once(lens, news, Hq, Hkv, d, page, dtype):
+    counted(lens, news, Hq=Hq, Hkv=Hkv, d=d, page=page, dtype=dtype)
+
+
+@pytest.mark.parametrize("window", [5, 100, 1000, 9000])
+def test_every_key_of_a_window_once(window):
+    counted([30000, 500], [1, 1], Hq=8, Hkv=2, d=128, page=16, dtype=torch.float16, window=window)
+    counted([30000, 500, 20000], [300, 1, 7], Hq=8, Hkv=2, d=128, page=16, dtype=torch.float16, window=window)
+
+
+def test_every_key_of_many_requests_once():
+    rng = random.Random(41)
+    lens = [rng.choice([1, 31, 32, 33, rng.randint(1, 9000)]) for _ in range(120)]
+    for top in (1, 60):
+        news = [min(n, rng.choice([1, 1, rng.randint(1, top)])) for n in lens]
+        counted(lens, news, Hq=4, Hkv=2, d=128, page=16, dtype=torch.float16, max_new=top)
