@@ -908,3 +908,102 @@ def test_every_key_of_many_requests_once():
     for top in (1, 60):
         news = [min(n, rng.choice([1, 1, rng.randint(1, top)])) for n in lens]
         counted(lens, news, Hq=4, Hkv=2, d=128, page=16, dtype=torch.float16, max_new=top)
+
+
+# ------------------------------------------------------------------------------- calls at the edges
+
+@pytest.mark.parametrize("max_new", [1, 5, 200])
+def test_a_step_without_tokens(max_new):
+    """Every request idle: nothing is written, nothing is reported."""
+    k, v, table = _paged.make_paged([300, 0, 20], 16, 2, 128, torch.bfloat16, "nhd", 2)
+    q = torch.randn(7, 8, 128, device="cuda").to(torch.bfloat16)
+    out, lse = torch.full_like(q, 3.0), torch.full((8, 7), 3.0, device="cuda")
+    fa.fa_paged_fwd(q, k, v, table, i32([0, 0, 0, 0]), i32([300, 0, 20]), max_new=max_new, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert bool((out == 3.0).all()) and bool((lse == 3.0).all())
+
+
+@pytest.mark.parametrize("news", [[1, 1], [1, 90]])
+def test_a_table_without_blocks(news):
+    """max_blocks = 0: requests of no keys alone; their rows see nothing."""
+    k = torch.randn(4, 16, 2, 64, device="cuda").to(torch.bfloat16)
+    q = torch.randn(sum(news), 4, 64, device="cuda").to(torch.bfloat16)
+    table = torch.zeros((2, 0), dtype=torch.int32, device="cuda")
+    out, lse = fa.fa_paged_fwd(q, k, k.clone(), table, i32([0, news[0], sum(news)]), i32([0, 0]), max_new=max(news))
+    assert not bool(out.any()) and bool((lse == -math.inf).all())
+
+
+@pytest.mark.parametrize("new", [1, 100])
+def test_one_page_for_all(new):
+    """A page longer than the request: a cache that is one array a request."""
+    attend([30000, 17], [new, 1], Hq=4, Hkv=2, d=64, page=40000, seed=new)
+
+
+def test_layers_that_share_tables():
+    """Two layers over one set of tables: one reserve, one release, each its own keys and values."""
+    torch.manual_seed(31)
+    inv, axis = spec(64, 1)
+    rope = fa.RopeTable(inv)
+    first = fa.PagedKV(3, 20, 16, 2, 64, max_blocks=10)
+    layers = [first, fa.PagedKV(3, 20, 16, 2, 64, tables=first, layout="hnd"), fa.PagedKV(3, 20, 16, 1, 128, tables=first, dtype=torch.float16)]
+    kept = [[], [], []]
+    lens = [0, 0, 0]
+    for step in ([40, 0, 9], [1, 30, 1], [1, 1, 1]):
+        T = sum(step)
+        first.reserve(i32(step), T)
+        lens = [a + b for a, b in zip(lens, step)]
+        cu = [0, step[0], step[0] + step[1], T]
+        for n, kv in enumerate(layers):
+            dt = kv.k_cache.dtype
+            q, k, v = (torch.randn(T, h, kv.d, device="cuda").to(dt) for h in (4, kv.Hkv, kv.Hkv))
+            kept[n].append((step, v))
+            table = rope if kv.d == 64 else fa.RopeTable(spec(128, 1)[0])
+            rows = kv.append(q, k, v, table)
+            out, lse = kv.attend(rows, max_new=max(step))
+            want, z, t_out, t_lse = _paged.attend64(rows, kv.k_cache, kv.v_cache, first.block_table, cu, lens, causal=True, window=None,
+                                                    scale=kv.d ** -0.5)
+            close(out, want, t_out)
+            close(lse, z, t_lse)
+    for n, kv in enumerate(layers):   # each layer holds its own values, request by request
+        for r in range(3):
+            mine = torch.cat([v[sum(s[:r]):sum(s[:r + 1])] for s, v in kept[n]])
+            pages = first.block_table[r, :_paged.blocks_of(lens[r], 16)].long()
+            assert torch.equal(kv.v_cache[pages].reshape(-1, kv.Hkv, kv.d)[:lens[r]], mine)
+    with pytest.raises(ValueError):
+        layers[1].reserve(i32([1, 1, 1]), 3)
+    with pytest.raises(ValueError):
+        layers[1].release(i32([1, 0, 0]))
+    first.release(i32([1, 1, 1]))
+    assert first.free_count.item() == 20 and sorted(first.free_blocks.tolist()) == list(range(20))
+
+
+@pytest.mark.parametrize("T", [500, 40000])
+def test_reserve_and_release_captured(T):
+    """Both updated in place in one graph, the many-token path among them: replays give what eager steps give."""
+    page, R = 16, 37
+    rng = random.Random(T)
+    new = [rng.randint(0, T // R) for _ in range(R)]
+    done = [rng.choice([0, 0, 1]) for _ in range(R)]
+
+    def start():
+        return dict(lens=torch.zeros(R, dtype=torch.int32, device="cuda"), table=torch.full((R, 4 * T // R // page + 8), -7, dtype=torch.int32, device="cuda"),
+                    stack=torch.arange(5 * T // page, dtype=torch.int32, device="cuda"), count=i32([5 * T // page]),
+                    cu=torch.zeros(R + 1, dtype=torch.int32, device="cuda"), pos=torch.zeros(T, dtype=torch.int32, device="cuda"),
+                    slots=torch.zeros(T, dtype=torch.int64, device="cuda"))
+    n, d = i32(new), i32(done)
+
+    def step(s):
+        fa.fa_kv_reserve(s["lens"], n, s["table"], s["stack"], s["count"], page_size=page, cu_seqlens=s["cu"], seq_lens=s["lens"], positions=s["pos"],
+                         slots=s["slots"], free_count_out=s["count"])
+        fa.fa_kv_release(s["lens"], d, s["table"], s["stack"], s["count"], page_size=page, lens_out=s["lens"], free_count_out=s["count"])
+    eager, graphed = start(), start()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        step(graphed)
+    for _ in range(3):
+        step(eager)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(eager[x], graphed[x]) for x in eager)
+    assert eager["lens"].tolist() == [0 if f else 3 * x for f, x in zip(done, new)]
