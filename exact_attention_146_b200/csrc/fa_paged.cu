@@ -101,9 +101,6 @@ struct View {
     int box[3];
 };
 
-// Chunks on the tensor cores; requests of at most `few` new tokens (few > 0) by the kernel of few rows
-// behind it, whose CTAs start as the tile kernel's end: those end up to a quarter of the time apart, and the
-// other's work fills that.
 // The caches as the tensor maps see them: the axes after d, the nearer of head and slot first.
 View cache_view(const PagedParams &p, int Hkv) {
     View kv{p.k, {Hkv, p.page, p.num_blocks}, {p.head_stride, p.slot_stride, p.block_stride}, {1, 1, 1}};
@@ -182,6 +179,9 @@ template <bool H> using Tile256 = TileCfg<256, 64, 1, 4, 1, 2, false, 0, H>;
 // (d = 64): 93, 97, 96 us with 2, 3, 4.
 constexpr int kTileOverhead = 2;
 
+// Chunks on the tensor cores; requests of at most `few` new tokens (few > 0) by the kernel of few rows
+// behind it, whose CTAs start as the tile kernel's end: those end up to a quarter of the time apart, and the
+// other's work fills that.
 template <class C, int FEW>
 int launch_tiles(const PagedParams &base, const View &q, const View &kv, int few, char *workspace, int ctas, int dev,
                  cudaStream_t st) {
@@ -316,8 +316,12 @@ int paged_fwd(const void *q, long long q_stride, const fa_paged_cache *given, co
     p.slot_first = p.slot_stride < p.head_stride ? 1 : 0;
     const View kv = cache_view(p, Hkv);
     char *const ws = static_cast<char *>(workspace);
-    // Row tiles of 128 need pages of whole swizzle atoms (8 slots); any other page, and calls of few rows,
-    // take the kernel that gathers key by key.  In a mixed call the requests of few rows take it too.
+    // Calls of up to 16 rows a KV head, and in a mixed call the requests of so few, take the kernel of few rows.  48
+    // requests of 4k to 16k keys (d 128), whose K and V cost 281 us at the copy rate: 4 rows 281 us, 16 rows 316 us;
+    // by the tile kernel 449 us for 20 rows and 457 us for 124.  (Two units of 16 rows would read K and V twice, 563 us.)
+    // Row tiles of 128 need pages of whole swizzle atoms (8 slots), so prompts over any other page take the kernel of
+    // few rows too, which reads K and V once per 16 rows: 4096 new tokens over 28672 keys (Hq 32, Hkv 8, d 128) take 40 ms
+    // with pages of 1, 4 or 100, against 1.71 ms with 128, 1.96 with 16, 2.85 with 8.
     const bool eight = p.n_rep <= 8;   // a unit of 8 rows holds a decoding step; else one of 16
     const int few = kRowRows / p.n_rep;   // new tokens whose rows fit a unit
     if (max_new > few && p.page % 8 == 0 && p.num_blocks > 0) {

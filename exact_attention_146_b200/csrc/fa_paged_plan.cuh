@@ -12,7 +12,8 @@
 //
 // The lengths are on the device, so every worker finds its own range.  The steps of a request are
 // a closed form: with A(c) = sum over blocks of floor(max(0, tpb b + c) / KS) (a floor sum, by the
-// Euclidean recursion), a group of nb blocks takes nb (1 + overhead) + A(tpb - 1 + L - n) -
+// Euclidean recursion that follows from the reciprocity of such sums: Graham, Knuth and Patashnik, Concrete
+// Mathematics, section 3.5), a group of nb blocks takes nb (1 + overhead) + A(tpb - 1 + L - n) -
 // A(L - n - W + 1) steps.  A block sums the requests once (each thread a contiguous segment of them), scans the
 // segment sums, and a worker finds its place by bisection.
 #pragma once

@@ -383,7 +383,8 @@ int fa_rope_append_f16(const void *q, long long q_stride, void *q_out, long long
  *
  * New token i of request r sees key j < L_r iff (causal = 0 or j <= i + L_r - n_r) and
  * (window = 0 or j > i + L_r - n_r - window); window > 0 needs causal = 1.  A row that sees no
- * key gets O = 0 and LSE = -inf.  Rows of out and lse outside every request are left as they are.
+ * key gets O = 0 and LSE = -inf; one whose sum of exponentials is NaN (NaN in q, overflow) gets O = LSE = NaN.
+ * Rows of out and lse outside every request are left as they are.
  * Only blocks that hold a visible key are looked up and read; slots of such a block behind L_r may hold
  * anything, NaN included.
  *
